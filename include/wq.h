@@ -387,7 +387,8 @@ size_t wq_gptq_workspace_bytes(int64_t d_out, int64_t d_in);
  * wq_get_device_error -- synchronize `stream`, read and clear the device
  * status word of the current device.  *flags receives the WQ_DEVFLAG_* bits
  * (may be NULL).  Returns WQ_OK when no bit was set, otherwise the status of
- * the most severe bit (TIMEOUT, then NONFINITE, then RANGE), or WQ_ERR_CUDA.
+ * the most severe bit (TIMEOUT, then NONFINITE, then RANGE, then the INDEX bit
+ * of wq_int8.h as WQ_ERR_INVALID_ARG), or WQ_ERR_CUDA.
  */
 wq_status wq_get_device_error(uint32_t* flags, void* stream);
 

@@ -1,0 +1,461 @@
+"""8-bit serving products on the GPU against their plain definition: codes and
+scales bit for bit, products bit for bit (integer sums, three fp32 roundings,
+one to bf16) and within those roundings of the 64-bit value."""
+import numpy as np
+import pytest
+import torch
+
+from tests import _int8_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _clear_status():
+    from w4a16_bit_gemm_b200 import binding
+    binding.device_error()
+    yield
+    st, flags = binding.device_error()
+    assert st == binding.WQ_OK, (st, flags)
+
+
+def _b():
+    from w4a16_bit_gemm_b200 import binding
+    return binding
+
+
+def activations(R, K, seed, spread=True):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(R, K, generator=g)
+    if spread:
+        x *= torch.exp(torch.randn(R, 1, generator=g) * 3)
+        x[:, torch.randperm(K, generator=g)[:1]] *= 50
+    return x.to(torch.bfloat16)
+
+
+def operands(R, N, K, seed, E=None):
+    """Random codes over the whole int8 range, fp16 weight scales, fp32 row scales."""
+    rng = np.random.default_rng(seed)
+    lead = () if E is None else (E,)
+    xq = rng.integers(-128, 128, (R, K), dtype=np.int8)
+    wq = rng.integers(-128, 128, lead + (N, K), dtype=np.int8)
+    xs = np.exp(rng.normal(-4, 2, R)).astype(np.float32)
+    ws = np.exp(rng.normal(-6, 1, lead + (N,))).astype(np.float16)
+    return xq, xs, wq, ws
+
+
+def tokens(xq, xs):
+    return _b().QuantizedTokens(torch.from_numpy(xq).cuda(), torch.from_numpy(xs).cuda())
+
+
+def dense(wq, ws):
+    N, K = wq.shape
+    return _b().PackedLinearW8(ref.words(wq).cuda(), torch.from_numpy(ws).cuda(), N, K, K)
+
+
+def experts(wq, ws):
+    return _b().PackedExpertsW8(ref.words(wq).cuda(), torch.from_numpy(ws).cuda())
+
+
+# ---------------------------------------------------------------------------
+# quantize_tokens
+# ---------------------------------------------------------------------------
+
+def check_tokens(X, rows=None, smooth=None):
+    b = _b()
+    x = X if rows is None else X[rows.long()]
+    if smooth is not None:
+        x = ref.smoothed(x, smooth)
+    q, s, bad = ref.quantize_tokens(x)
+    got = b.quantize_tokens(X.cuda(), None if rows is None else rows.cuda(), None if smooth is None else smooth.cuda())
+    assert np.array_equal(got.scales.cpu().numpy().view(np.uint32), s.view(np.uint32))
+    assert np.array_equal(got.codes.cpu().numpy(), q)
+    st, flags = b.device_error()
+    assert flags == (b.WQ_DEVFLAG_NONFINITE if bad else 0)
+
+
+# every kernel variant: row lengths on both sides of each thread count, register-held and re-read
+@pytest.mark.parametrize("K", [32, 96, 256, 1024, 1056, 2048, 2080, 4096, 4128, 8192, 8224, 11008, 16384, 16416, 20000])
+@pytest.mark.parametrize("R", [1, 2, 9])
+def test_tokens_match_definition(K, R):
+    check_tokens(activations(R, K, K + R))
+
+
+def test_tokens_many_rows():
+    check_tokens(activations(3000, 512, 5))
+    check_tokens(activations(700, 4096, 6))
+
+
+def test_tokens_values_on_and_next_to_ties():
+    # amax = 127 * 2^j: x / s is exact, so half-integers are exact ties; the row
+    # holds every bf16 value of [2^j / 4, 127 * 2^j]
+    bits = np.arange(0x3e80, 0x42ff, dtype=np.uint16)  # 0.25 ... 127.5
+    v = torch.from_numpy(bits.view(np.int16)).view(torch.bfloat16).float()
+    v = v[v <= 127]
+    rows = []
+    for j in (-130, -100, -3, 0, 5, 100):
+        x = torch.cat([v, -v, torch.full((32 - (2 * len(v)) % 32,), 127.0)])
+        rows.append(x * 2.0 ** j)
+    check_tokens(torch.stack(rows).to(torch.bfloat16))
+    # other maxima: 127 of them, so that ties and near-ties fall everywhere
+    top = torch.from_numpy(np.arange(0x42c0, 0x42ff, dtype=np.uint16).view(np.int16)).view(torch.bfloat16).float()
+    n = 32 * (len(v) // 32)
+    check_tokens(torch.cat([top[:, None], v[None, :n - 1].clamp(max=90).expand(len(top), -1)], 1).to(torch.bfloat16))
+
+
+def test_tokens_tiny_huge_and_zero_rows():
+    x = torch.randn(8, 288, generator=torch.Generator().manual_seed(1))
+    x[0] = 0
+    x[1] *= 2.0 ** -133      # subnormal bf16, subnormal scale
+    x[2] *= 2.0 ** -126
+    x[3] *= 2.0 ** -118      # on both sides of the scale where the reciprocal is used
+    x[4] *= 2.0 ** -112
+    x[5] *= 2.0 ** 124
+    x[6] = -0.0
+    x[7, 1:] = 0
+    check_tokens(x.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("K", [64, 1056, 4096, 16416])
+def test_tokens_nonfinite(K):
+    x = activations(9, K, 8).float()
+    x[1, 3] = float("nan")
+    x[2, K - 1] = float("inf")
+    x[3, 7] = -float("inf")
+    x[4] = float("nan")
+    x[5] = float("inf")
+    x[5, 4] = 3.0
+    x[7, ::2] = float("nan")
+    check_tokens(x.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("K", [32, 1056, 4096, 16416])
+def test_tokens_smoothed_and_gathered(K):
+    X = activations(13, K, 9)
+    g = torch.Generator().manual_seed(4)
+    smooth = (torch.rand(K, generator=g) * 8 + 0.01).to(torch.bfloat16)
+    rows = torch.randint(0, 13, (57,), generator=g).to(torch.int32)
+    check_tokens(X, smooth=smooth)
+    check_tokens(X, rows=rows)
+    check_tokens(X, rows=rows, smooth=smooth)
+    # the smoothed values are awq_scale_activations' own
+    b = _b()
+    a = b.quantize_tokens(b.awq_scale_activations(X.cuda(), smooth.cuda()))
+    c = b.quantize_tokens(X.cuda(), smooth=smooth.cuda())
+    assert torch.equal(a.codes, c.codes) and torch.equal(a.scales, c.scales)
+
+
+def test_tokens_smoothing_at_the_ends_of_the_range():
+    K = 256
+    X = activations(6, K, 10).float()
+    X[1] *= 2.0 ** -120
+    X[2] *= 2.0 ** 100
+    smooth = torch.ones(K)
+    smooth[::7] = 2.0 ** -60
+    smooth[1::7] = 2.0 ** 60
+    smooth[2::7] = -3.0
+    smooth[3::7] = 2.0 ** -133
+    smooth[4::7] = 3e38
+    check_tokens(X.to(torch.bfloat16), smooth=smooth.to(torch.bfloat16))
+
+
+def test_tokens_bad_row_index_is_flagged_and_coded_zero():
+    b = _b()
+    X = activations(5, 128, 11)
+    rows = torch.tensor([0, 5, 4, -1, 2, 1 << 30], dtype=torch.int32)
+    got = b.quantize_tokens(X.cuda(), rows.cuda(), torch.ones(128, dtype=torch.bfloat16).cuda())
+    st, flags = b.device_error()
+    assert st == b.WQ_ERR_INVALID_ARG and flags == b.WQ_DEVFLAG_INDEX
+    q, s, _ = ref.quantize_tokens(X[rows.clamp(0, 4).long()])
+    dead = ((rows < 0) | (rows >= 5)).numpy()
+    q[dead], s[dead] = 0, 1
+    assert np.array_equal(got.codes.cpu().numpy(), q) and np.array_equal(got.scales.cpu().numpy(), s)
+
+
+# ---------------------------------------------------------------------------
+# linear_w8a8
+# ---------------------------------------------------------------------------
+
+def check_linear(M, N, K, seed=0, dtype=torch.bfloat16):
+    xq, xs, wq, ws = operands(M, N, K, seed)
+    y, y64 = ref.product(xq, xs, wq, ws)
+    ref.check(_b().linear_w8a8(tokens(xq, xs), dense(wq, ws), out_dtype=dtype), y, y64)
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 8, 15, 16, 17, 31, 33, 64, 65])
+@pytest.mark.parametrize("N,K", [(1, 32), (37, 96), (128, 128), (129, 416), (1000, 1056), (301, 4096)])
+def test_linear_few_tokens(M, N, K):
+    check_linear(M, N, K, M + N + K, torch.float32 if (M + N) % 2 else torch.bfloat16)
+
+
+@pytest.mark.parametrize("M,N,K", [(127, 300, 160), (128, 640, 512), (129, 257, 1056), (255, 128, 96), (256, 1000, 288),
+                                   (257, 255, 2080), (300, 1001, 1056), (513, 600, 128), (777, 1409, 544),
+                                   (1030, 2049, 1024), (2500, 513, 256)])
+def test_linear_many_tokens(M, N, K):
+    check_linear(M, N, K, M, torch.float32 if N % 2 else torch.bfloat16)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (5, 4096, 11008), (16, 11008, 4096), (3, 28672, 256),
+                                   (40, 4096, 4096)])
+def test_linear_decode_shapes(M, N, K):
+    check_linear(M, N, K, 3)
+
+
+@pytest.mark.parametrize("M", [2, 300])
+def test_linear_deepest_sum_does_not_wrap(M):
+    K, N = 131040, 130
+    xq, wq = np.full((M, K), -128, np.int8), np.full((N, K), -128, np.int8)
+    wq[1] = 127
+    y, y64 = ref.product(xq, np.ones(M, np.float32), wq, np.ones(N, np.float16))
+    ref.check(_b().linear_w8a8(tokens(xq, np.ones(M, np.float32)), dense(wq, np.ones(N, np.float16)),
+                               out_dtype=torch.float32), y, y64)
+    assert y64[0, 0] == 128 * 128 * K
+
+
+def test_linear_scales_at_the_ends_of_the_range():
+    xq, xs, wq, ws = operands(6, 200, 256, 1)
+    xs[:] = [3e36, 1e-45, 1e-38, 0.0, float("inf"), float("nan")]
+    ws[:4] = [65504, 6e-8, 0.0, 1.0]
+    wq[5] = 0
+    y, _ = ref.product(xq, xs, wq, ws)
+    got = _b().linear_w8a8(tokens(xq, xs), dense(wq, ws), out_dtype=torch.float32).cpu().numpy()
+    assert np.array_equal(got, y, equal_nan=True)
+
+
+def test_linear_whole_path_from_bf16():
+    """quantize_w8 weights, bf16 activations with smoothing: the two calls and
+    the one call agree with the definition."""
+    b = _b()
+    W = (torch.randn(333, 1056, generator=torch.Generator().manual_seed(2)) * 0.02).to(torch.bfloat16)
+    X = activations(21, 1056, 12, spread=False)
+    smooth = (X.float().abs().mean(0) + 0.1).sqrt().to(torch.bfloat16)
+    p = b.quantize_w8(W.cuda())
+    xq, xs, _ = ref.quantize_tokens(ref.smoothed(X, smooth))
+    wq = p.qweight.cpu().view(torch.int8).numpy()
+    y, y64 = ref.product(xq, xs, wq, p.scales.cpu().numpy()[:, 0])
+    one = b.linear_w8a8(X.cuda(), p, smooth=smooth.cuda(), out_dtype=torch.float32)
+    ref.check(one, y, y64)
+    two = b.linear_w8a8(b.quantize_tokens(X.cuda(), smooth=smooth.cuda()), p, out_dtype=torch.float32)
+    assert torch.equal(one, two)
+
+
+def test_linear_no_tokens():
+    b = _b()
+    _, _, wq, ws = operands(1, 40, 64, 0)
+    x = b.quantize_tokens(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"))
+    assert b.linear_w8a8(x, dense(wq, ws)).shape == (0, 40)
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    assert b.linear_w8a8_grouped(x, experts(wq[None], ws[None]), off).shape == (0, 40)
+
+
+# ---------------------------------------------------------------------------
+# linear_w8a8_grouped
+# ---------------------------------------------------------------------------
+
+def check_grouped(counts, N, K, seed=0, dtype=torch.bfloat16, before=0, behind=0):
+    E = len(counts)
+    R = before + sum(counts) + behind
+    offsets = np.concatenate([[0], np.cumsum(counts)]) + before
+    xq, xs, wq, ws = operands(R, N, K, seed, E)
+    held = torch.randn(R, N, generator=torch.Generator().manual_seed(seed)).to(dtype)
+    y, y64 = ref.grouped(xq, xs, wq, ws, offsets, held)
+    out = held.cuda()
+    got = _b().linear_w8a8_grouped(tokens(xq, xs), experts(wq, ws),
+                                   torch.from_numpy(offsets.astype(np.int32)).cuda(), out=out)
+    assert got is out
+    ref.check(out, y, y64)
+
+
+@pytest.mark.parametrize("counts", [
+    [1], [0, 1], [1, 0, 0], [0, 0, 0], [1] * 40, [16, 17, 15], [0, 33, 0, 64, 1], [100, 0, 3], [5, 250, 1],
+    [257, 0, 513, 31], [2000, 1], [0] * 30 + [70] + [0] * 30,
+], ids=lambda c: "-".join(map(str, c))[:24])
+@pytest.mark.parametrize("N,K", [(70, 96), (257, 1056)])
+def test_grouped_counts(counts, N, K):
+    check_grouped(counts, N, K, len(counts) + N, torch.float32 if N % 2 else torch.bfloat16)
+
+
+@pytest.mark.parametrize("E", [2, 191, 192, 193, 400, 1024])
+def test_grouped_many_experts(E):
+    rng = np.random.default_rng(E)
+    check_grouped(rng.integers(0, 4, E).tolist(), 36, 64, E)
+
+
+def test_grouped_skewed_prompt():
+    rng = np.random.default_rng(7)
+    check_grouped(rng.multinomial(1500, rng.dirichlet(np.full(24, 0.4))).tolist(), 640, 512, 7)
+
+
+def test_grouped_leaves_other_rows_as_they_were():
+    check_grouped([3, 0, 20], 130, 160, 1, before=7, behind=9)
+    check_grouped([300, 280], 130, 160, 2, torch.float32, before=1, behind=300)
+    check_grouped([0, 0], 130, 160, 3, before=4, behind=4)
+
+
+@pytest.mark.parametrize("offsets", [[0, 5, 3, 8], [-4, 2, 9, 10], [0, 4, 40, 50], [9, 2, 1, 0], [50, 60, 70, 80],
+                                     [-9, -8, -7, -6], [0, 0, 10, 2]])
+def test_grouped_bad_offsets_are_flagged_and_stay_in_bounds(offsets):
+    b = _b()
+    R, N, K = 10, 140, 64
+    xq, xs, wq, ws = operands(R, N, K, 3, 3)
+    held = torch.randn(R, N, generator=torch.Generator().manual_seed(1))
+    taken = np.maximum.accumulate(np.clip(offsets, 0, R))
+    y, y64 = ref.grouped(xq, xs, wq, ws, taken, held)
+    got = b.linear_w8a8_grouped(tokens(xq, xs), experts(wq, ws), torch.tensor(offsets, dtype=torch.int32).cuda(),
+                                out=held.cuda())
+    st, flags = b.device_error()
+    assert st == b.WQ_ERR_INVALID_ARG and flags == b.WQ_DEVFLAG_INDEX
+    ref.check(got, y, y64)
+
+
+def test_grouped_equals_dense_per_expert():
+    b = _b()
+    W = (torch.randn(3, 200, 288, generator=torch.Generator().manual_seed(5)) * 0.02).to(torch.bfloat16).cuda()
+    X = activations(50, 288, 13).cuda()
+    p = b.quantize_w8_experts(W)
+    off = torch.tensor([0, 12, 12, 50], dtype=torch.int32, device="cuda")
+    y = b.linear_w8a8_grouped(X, p, off, out_dtype=torch.float32)
+    for e in (0, 2):
+        lo, hi = int(off[e]), int(off[e + 1])
+        assert torch.equal(y[lo:hi], b.linear_w8a8(X[lo:hi].contiguous(), b.quantize_w8(W[e]), out_dtype=torch.float32))
+
+
+# ---------------------------------------------------------------------------
+# Used together, streams, graphs
+# ---------------------------------------------------------------------------
+
+def expert_layer(b, X, up, down, rows, offsets, smooth):
+    """Tokens to their experts: up product, relu squared, down product."""
+    h = b.linear_w8a8_grouped(X, up, offsets, rows=rows, smooth=smooth)
+    h = torch.relu(h).square()
+    return b.linear_w8a8_grouped(h, down, offsets, out_dtype=torch.float32)
+
+
+def expert_layer_case(seed=0, T=37, top=2, E=6, d=256, f=416):
+    b = _b()
+    g = torch.Generator().manual_seed(seed)
+    up = b.quantize_w8_experts((torch.randn(E, f, d, generator=g) * 0.05).to(torch.bfloat16).cuda())
+    down = b.quantize_w8_experts((torch.randn(E, d, f, generator=g) * 0.05).to(torch.bfloat16).cuda())
+    X = torch.randn(T, d, generator=g).to(torch.bfloat16)
+    choice = torch.stack([torch.randperm(E, generator=g)[:top] for _ in range(T)])
+    order = torch.argsort(choice.flatten(), stable=True)
+    rows = (order // top).to(torch.int32)
+    offsets = torch.nn.functional.pad(torch.bincount(choice.flatten(), minlength=E).cumsum(0), (1, 0)).to(torch.int32)
+    smooth = (torch.rand(d, generator=g) + 0.5).to(torch.bfloat16)
+    return X, up, down, rows, offsets, smooth
+
+
+def expert_layer_ref(X, up, down, rows, offsets, smooth):
+    wq = [p.qweight.cpu().view(torch.int8).numpy() for p in (up, down)]
+    ws = [p.scales.cpu().numpy() for p in (up, down)]
+    xq, xs, _ = ref.quantize_tokens(ref.smoothed(X[rows.long()], smooth))
+    held = torch.zeros(len(rows), wq[0].shape[1])
+    h, _ = ref.grouped(xq, xs, wq[0], ws[0], offsets.tolist(), held)
+    h = torch.relu(torch.from_numpy(h).to(torch.bfloat16)).square()
+    xq, xs, _ = ref.quantize_tokens(h)
+    return ref.grouped(xq, xs, wq[1], ws[1], offsets.tolist(), torch.zeros(len(rows), wq[1].shape[1]))
+
+
+def test_expert_layer_end_to_end():
+    b = _b()
+    for seed, T, top, E in ((0, 37, 2, 6), (1, 1, 2, 8), (2, 300, 4, 5)):
+        X, up, down, rows, offsets, smooth = expert_layer_case(seed, T, top, E)
+        y, y64 = expert_layer_ref(X, up, down, rows, offsets, smooth)
+        ref.check(expert_layer(b, X.cuda(), up, down, rows.cuda(), offsets.cuda(), smooth.cuda()), y, y64)
+
+
+def test_expert_layer_captured_and_replayed_on_new_inputs():
+    b = _b()
+    X, up, down, rows, offsets, smooth = expert_layer_case(3)
+    buf = [t.cuda() for t in (X, rows, offsets, smooth)]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        for _ in range(2):
+            expert_layer(b, buf[0], up, down, buf[1], buf[2], buf[3])
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = expert_layer(b, buf[0], up, down, buf[1], buf[2], buf[3])
+    for seed in (4, 5):
+        X2, _, _, rows2, offsets2, smooth2 = expert_layer_case(seed)
+        for dst, src in zip(buf, (X2, rows2, offsets2, smooth2)):
+            dst.copy_(src)
+        graph.replay()
+        y, y64 = expert_layer_ref(X2, up, down, rows2, offsets2, smooth2)
+        ref.check(out, y, y64)
+
+
+def test_back_to_back_launches_keep_their_order():
+    """A chain of dependent layers, many times over: each kernel may start
+    before the one ahead of it ends, and must not read or write too early."""
+    b = _b()
+    g = torch.Generator().manual_seed(6)
+    p = b.quantize_w8((torch.randn(512, 512, generator=g) * 0.05).to(torch.bfloat16).cuda())
+    for M in (1, 20, 300):
+        x = torch.randn(M, 512, generator=g).to(torch.bfloat16).cuda()
+        buf = [torch.empty_like(x) for _ in range(2)]
+        first = None
+        for _ in range(20):
+            cur = x
+            for i in range(12):
+                cur = b.linear_w8a8(cur, p, out=buf[i % 2])
+            first = cur.clone() if first is None else first
+            assert torch.equal(cur, first)
+        cur = x
+        for i in range(12):
+            torch.cuda.synchronize()
+            cur = b.linear_w8a8(cur, p).clone()
+        assert torch.equal(cur, first)
+
+
+def test_two_streams_at_once():
+    b = _b()
+    cases = []
+    for i in range(2):
+        xq, xs, wq, ws = operands(9 + 200 * i, 700, 1056, i)
+        cases.append((tokens(xq, xs), dense(wq, ws), ref.product(xq, xs, wq, ws)))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            outs[i].append(b.linear_w8a8(cases[i][0], cases[i][1], out_dtype=torch.float32, stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in outs[i]:
+            ref.check(o, *cases[i][2])
+
+
+def test_binding_refuses():
+    b = _b()
+    xq, xs, wq, ws = operands(4, 64, 128, 0)
+    x, p, pe = tokens(xq, xs), dense(wq, ws), experts(wq[None], ws[None])
+    off = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    X = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
+    ok = torch.empty(4, 64, dtype=torch.bfloat16, device="cuda")
+    per_group = b.quantize_w8(torch.randn(64, 128, device="cuda").to(torch.bfloat16), 32)
+    bad = [
+        lambda: b.linear_w8a8(x, per_group),
+        lambda: b.linear_w8a8(X.float(), p),
+        lambda: b.linear_w8a8(X[:, :96].contiguous(), p),
+        lambda: b.linear_w8a8(X.t().contiguous().t(), p),
+        lambda: b.linear_w8a8(x, p, smooth=torch.ones(128, dtype=torch.bfloat16, device="cuda")),
+        lambda: b.linear_w8a8(X, p, smooth=torch.ones(64, dtype=torch.bfloat16, device="cuda")),
+        lambda: b.linear_w8a8(x, p, out_dtype=torch.float16),
+        lambda: b.linear_w8a8(x, p, out=ok, out_dtype=torch.float32),
+        lambda: b.linear_w8a8(x, p, out=ok[:3]),
+        lambda: b.linear_w8a8(x, p, out=ok.half()),
+        lambda: b.linear_w8a8(b.QuantizedTokens(x.codes, x.scales[:3]), p),
+        lambda: b.linear_w8a8(b.QuantizedTokens(x.codes.int(), x.scales), p),
+        lambda: b.linear_w8a8_grouped(x, pe, off.long()),
+        lambda: b.linear_w8a8_grouped(x, pe, off[:1]),
+        lambda: b.linear_w8a8_grouped(x, pe, off.cpu()),
+        lambda: b.linear_w8a8_grouped(x, pe, off, rows=off),
+        lambda: b.linear_w8a8_grouped(X, pe, off, rows=off.long()),
+        lambda: b.quantize_tokens(X, out=b.QuantizedTokens(x.codes[:2], x.scales)),
+        lambda: b.quantize_tokens(X, rows=off.view(2, 1)),
+    ]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()

@@ -1,4 +1,4 @@
-"""Thin ctypes binding of libwq (include/wq.h).
+"""Thin ctypes binding of libwq (include/wq.h, include/wq_int8.h).
 
 Argument marshalling only: every step of quantize, dequantize and the W4A16
 linear layer runs in the CUDA kernels of libwq.so.  PyTorch supplies device
@@ -26,6 +26,7 @@ WQ_ERR_RANGE = 6
 WQ_DEVFLAG_NONFINITE = 0x1
 WQ_DEVFLAG_RANGE = 0x2
 WQ_DEVFLAG_TIMEOUT = 0x4
+WQ_DEVFLAG_INDEX = 0x8
 
 WQ_OUT_BF16 = 0
 WQ_OUT_FP32 = 1
@@ -78,6 +79,12 @@ def _load() -> ctypes.CDLL:
     lib.wq_gptq.restype = ctypes.c_int
     lib.wq_gptq_workspace_bytes.argtypes = [i64, i64]
     lib.wq_gptq_workspace_bytes.restype = sz
+    lib.wq_quantize_tokens.argtypes = [P, i64, i64, P, i64, P, P, P, P]
+    lib.wq_quantize_tokens.restype = ctypes.c_int
+    lib.wq_linear_w8a8.argtypes = [P, P, i64, P, P, i64, i64, P, i32, P]
+    lib.wq_linear_w8a8.restype = ctypes.c_int
+    lib.wq_linear_w8a8_grouped.argtypes = [P, P, i64, P, i64, P, P, i64, i64, P, i32, P]
+    lib.wq_linear_w8a8_grouped.restype = ctypes.c_int
     lib.wq_get_device_error.argtypes = [P, P]
     lib.wq_get_device_error.restype = ctypes.c_int
     lib.wq_selftest_bounded_wait.argtypes = [ctypes.c_uint32, P]
@@ -174,6 +181,21 @@ def wq_dequantize_w8(qweight, scales, d_out, d_in, group_size, W_hat, stream=Non
 def wq_linear_w8a16(X, M, qweight, scales, d_out, d_in, group_size, Y, y_dtype, stream=None) -> int:
     return lib.wq_linear_w8a16(_ptr(X), M, _ptr(qweight), _ptr(scales), d_out, d_in, group_size, _ptr(Y), y_dtype,
                                _stream(stream))
+
+
+def wq_quantize_tokens(X, T, d_in, rows, R, smooth, Xq, x_scales, stream=None) -> int:
+    return lib.wq_quantize_tokens(_ptr(X), T, d_in, _ptr(rows), R, _ptr(smooth), _ptr(Xq), _ptr(x_scales),
+                                  _stream(stream))
+
+
+def wq_linear_w8a8(Xq, x_scales, M, qweight, scales, d_out, d_in, Y, y_dtype, stream=None) -> int:
+    return lib.wq_linear_w8a8(_ptr(Xq), _ptr(x_scales), M, _ptr(qweight), _ptr(scales), d_out, d_in, _ptr(Y), y_dtype,
+                              _stream(stream))
+
+
+def wq_linear_w8a8_grouped(Xq, x_scales, R, offsets, E, qweight, scales, d_out, d_in, Y, y_dtype, stream=None) -> int:
+    return lib.wq_linear_w8a8_grouped(_ptr(Xq), _ptr(x_scales), R, _ptr(offsets), E, _ptr(qweight), _ptr(scales),
+                                      d_out, d_in, _ptr(Y), y_dtype, _stream(stream))
 
 
 def wq_gptq(W, d_out, d_in, X, T, group_size, symmetric, act_order, qweight, scales, zeros, perm, workspace,
@@ -316,6 +338,174 @@ def linear_w8a16(X: torch.Tensor, p: PackedLinearW8, out_dtype=torch.bfloat16, o
                           device=X.device)
     _check(wq_linear_w8a16(X, X.shape[0], p.qweight, p.scales, p.d_out, p.d_in, p.group_size, out, y_dtype, stream),
            "wq_linear_w8a16")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# 8-bit serving products (W8A8)
+# ---------------------------------------------------------------------------
+
+class QuantizedTokens:
+    """INT8 activations: codes int8 [rows, d_in] and one fp32 scale per row."""
+
+    def __init__(self, codes, scales):
+        self.codes = codes
+        self.scales = scales
+
+
+class PackedExpertsW8:
+    """Per-channel INT8 weights of E experts of one shape: qweight int32
+    [E, d_out, d_in / 4] (layout w8 v1 per expert), scales fp16 [E, d_out]."""
+
+    def __init__(self, qweight, scales):
+        self.qweight = qweight
+        self.scales = scales
+        self.experts, self.d_out, words = qweight.shape
+        self.d_in = words * 4
+
+    def nbytes(self) -> int:
+        return self.qweight.numel() * 4 + self.scales.numel() * 2
+
+
+def quantize_w8_experts(W: torch.Tensor, stream=None) -> PackedExpertsW8:
+    """Per-channel INT8 quantization (quantize_w8) of bf16 W[E, d_out, d_in]."""
+    _require_cuda(W)
+    if W.dtype != torch.bfloat16 or W.dim() != 3 or not W.is_contiguous():
+        raise ValueError("W must be a contiguous [E, d_out, d_in] bf16 CUDA tensor")
+    E, d_out, d_in = W.shape
+    with _on(W, stream):
+        p = quantize_w8(W.view(E * d_out, d_in), stream=stream)
+    return PackedExpertsW8(p.qweight.view(E, d_out, d_in // 4), p.scales.view(E, d_out))
+
+
+class _nothing:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NOTHING = _nothing()
+
+
+def _on(t: torch.Tensor, stream=None):
+    """Context in which work on `t` is queued: its device is the current one
+    and allocations belong to `stream` (the current stream when None)."""
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError("stream and tensors are on different devices")
+        return torch.cuda.stream(stream)
+    if t.device.index != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return _NOTHING
+
+
+def _expect(what: str, t: torch.Tensor, dtype, shape, device):
+    """Raise unless t is a contiguous tensor of this type and shape on `device`."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def quantize_tokens(X: torch.Tensor, rows: torch.Tensor | None = None, smooth: torch.Tensor | None = None,
+                    out: QuantizedTokens | None = None, stream=None) -> QuantizedTokens:
+    """INT8 codes of bf16 activations X[T, d_in], one scale per token.
+
+    rows (int32 [R], device): output row r holds token rows[r].  smooth (bf16
+    [d_in]): X / smooth is quantized (awq_scale_activations on the way)."""
+    if X.dtype != torch.bfloat16 or X.dim() != 2 or not X.is_contiguous():
+        raise ValueError("X must be a contiguous [T, d_in] bf16 CUDA tensor")
+    _require_cuda(X)
+    T, d_in = X.shape
+    R = T
+    if rows is not None:
+        R = rows.shape[0] if rows.dim() == 1 else -1
+        _expect("rows", rows, torch.int32, (R,), X.device)
+    if smooth is not None:
+        _expect("smooth", smooth, torch.bfloat16, (d_in,), X.device)
+    with _on(X, stream):
+        if out is None:
+            out = QuantizedTokens(torch.empty((R, d_in), dtype=torch.int8, device=X.device),
+                                  torch.empty((R,), dtype=torch.float32, device=X.device))
+        else:
+            _expect("out.codes", out.codes, torch.int8, (R, d_in), X.device)
+            _expect("out.scales", out.scales, torch.float32, (R,), X.device)
+        _check(wq_quantize_tokens(X, T, d_in, rows, R, smooth, out.codes, out.scales, stream), "wq_quantize_tokens")
+    return out
+
+
+def _w8a8_operands(x, rows, smooth, d_in, device, stream):
+    """The INT8 activations of a product: given, or quantized from bf16."""
+    if isinstance(x, QuantizedTokens):
+        if rows is not None or smooth is not None:
+            raise ValueError("rows and smooth apply to bf16 activations; these are quantized already")
+        R = x.codes.shape[0]
+        _expect("x.codes", x.codes, torch.int8, (R, d_in), device)
+        _expect("x.scales", x.scales, torch.float32, (R,), device)
+        return x
+    if x.dim() != 2 or x.shape[1] != d_in or x.device != device:
+        raise ValueError(f"x must be a contiguous [tokens, {d_in}] bf16 tensor on {device}")
+    return quantize_tokens(x, rows, smooth, stream=stream)
+
+
+def _w8a8_output(out, out_dtype, shape, device):
+    if out is None:
+        out_dtype = out_dtype or torch.bfloat16
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+        out = torch.empty(shape, dtype=out_dtype, device=device)
+    else:
+        if out.dtype not in (torch.bfloat16, torch.float32) or (out_dtype or out.dtype) != out.dtype:
+            raise ValueError("out must be a bf16 or fp32 tensor (of out_dtype, when both are given)")
+        _expect("out", out, out.dtype, shape, device)
+    return out, (WQ_OUT_FP32 if out.dtype == torch.float32 else WQ_OUT_BF16)
+
+
+def linear_w8a8(x, p: PackedLinearW8, out_dtype=None, out: torch.Tensor | None = None,
+                smooth: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y[M, d_out] = s_m w_n sum_k xq[m, k] q[n, k], INT8 x INT8 with exact
+    integer sums; p has one scale per output channel (quantize_w8's default).
+
+    x: QuantizedTokens, or bf16 activations [M, d_in], which are quantized
+    first (smooth as in quantize_tokens).  Layers that share their input
+    (q, k and v; gate and up) should quantize it once."""
+    device = p.qweight.device
+    _require_cuda(p.qweight)
+    if p.group_size != p.d_in:
+        raise ValueError("linear_w8a8 takes per-channel weights (quantize_w8 without a group_size)")
+    _expect("p.qweight", p.qweight, torch.int32, (p.d_out, p.d_in // 4), device)
+    _expect("p.scales", p.scales, torch.float16, (p.d_out,) if p.scales.dim() == 1 else (p.d_out, 1), device)
+    with _on(p.qweight, stream):
+        x = _w8a8_operands(x, None, smooth, p.d_in, device, stream)
+        M = x.codes.shape[0]
+        out, y_dtype = _w8a8_output(out, out_dtype, (M, p.d_out), device)
+        _check(wq_linear_w8a8(x.codes, x.scales, M, p.qweight, p.scales, p.d_out, p.d_in, out, y_dtype, stream),
+               "wq_linear_w8a8")
+    return out
+
+
+def linear_w8a8_grouped(x, p: PackedExpertsW8, offsets: torch.Tensor, out_dtype=None, out: torch.Tensor | None = None,
+                        rows: torch.Tensor | None = None, smooth: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """linear_w8a8 with one weight matrix per expert: rows offsets[e] ..
+    offsets[e + 1] - 1 of the activations are multiplied by expert e's matrix.
+
+    offsets: int32 [E + 1] on the device, non-decreasing, within [0, R].  x:
+    QuantizedTokens with R rows sorted by expert, or bf16 tokens, of which
+    rows (int32 [R]) names the one that each row takes.  Rows outside
+    [offsets[0], offsets[E]) of the output are not written."""
+    device = p.qweight.device
+    _require_cuda(p.qweight)
+    E = p.experts
+    _expect("p.qweight", p.qweight, torch.int32, (E, p.d_out, p.d_in // 4), device)
+    _expect("p.scales", p.scales, torch.float16, (E, p.d_out), device)
+    _expect("offsets", offsets, torch.int32, (E + 1,), device)
+    with _on(p.qweight, stream):
+        x = _w8a8_operands(x, rows, smooth, p.d_in, device, stream)
+        R = x.codes.shape[0]
+        out, y_dtype = _w8a8_output(out, out_dtype, (R, p.d_out), device)
+        _check(wq_linear_w8a8_grouped(x.codes, x.scales, R, offsets, E, p.qweight, p.scales, p.d_out, p.d_in, out,
+                                      y_dtype, stream), "wq_linear_w8a8_grouped")
     return out
 
 

@@ -37,7 +37,7 @@ def sources():
 
 def headers():
     hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    hs.append(os.path.join(INCLUDE, "wq.h"))
+    hs += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     return hs
 
 

@@ -14,6 +14,7 @@
 #include <mutex>
 
 #include "../../include/wq.h"
+#include "w8a8.h"
 #include "wq_kernels.h"
 
 namespace wq {
@@ -103,6 +104,17 @@ wq_status check_artifact(const void* qweight, const void* scales, const void* ze
     return WQ_OK;
 }
 
+}  // namespace
+
+wq_status device_info(uint32_t** status, int* num_sms) {
+    DeviceState st;
+    const wq_status v = device_state(&st);
+    if (v != WQ_OK) return v;
+    *status = st.status;
+    *num_sms = st.num_sms;
+    return WQ_OK;
+}
+
 bool pdl_enabled() {
     static int v = -1;
     if (v < 0) {
@@ -111,8 +123,6 @@ bool pdl_enabled() {
     }
     return v == 1;
 }
-
-}  // namespace
 
 bool gemv_tc_disabled() {
     static int v = -1;
@@ -571,6 +581,7 @@ wq_status wq_get_device_error(uint32_t* flags, void* stream) {
     if (h & WQ_DEVFLAG_TIMEOUT) return WQ_ERR_TIMEOUT;
     if (h & WQ_DEVFLAG_NONFINITE) return WQ_ERR_NONFINITE;
     if (h & WQ_DEVFLAG_RANGE) return WQ_ERR_RANGE;
+    if (h & WQ_DEVFLAG_INDEX) return WQ_ERR_INVALID_ARG;
     return WQ_OK;
 }
 
