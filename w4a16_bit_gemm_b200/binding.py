@@ -367,53 +367,47 @@ class PackedExpertsW8:
         return self.qweight.numel() * 4 + self.scales.numel() * 2
 
 
+def _elsewhere(device, stream):
+    """None when a call for tensors on `device` can be queued as things stand:
+    the device is the current one and no stream is named.  Otherwise a context
+    that makes it so (allocations then belong to that stream)."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("stream and tensors are on different devices")
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return None
+
+
+# The current stream's handle without building a Stream object (3 us a call).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _expect(what: str, t: torch.Tensor, dtype, shape, device):
+    """Raise unless t is a contiguous tensor of this type and shape on `device`."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
 def quantize_w8_experts(W: torch.Tensor, stream=None) -> PackedExpertsW8:
     """Per-channel INT8 quantization (quantize_w8) of bf16 W[E, d_out, d_in]."""
     _require_cuda(W)
     if W.dtype != torch.bfloat16 or W.dim() != 3 or not W.is_contiguous():
         raise ValueError("W must be a contiguous [E, d_out, d_in] bf16 CUDA tensor")
+    there = _elsewhere(W.device, stream)
+    if there is not None:
+        with there:
+            return quantize_w8_experts(W)
     E, d_out, d_in = W.shape
-    with _on(W, stream):
-        p = quantize_w8(W.view(E * d_out, d_in), stream=stream)
+    p = quantize_w8(W.view(E * d_out, d_in))
     return PackedExpertsW8(p.qweight.view(E, d_out, d_in // 4), p.scales.view(E, d_out))
 
 
-class _nothing:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_NOTHING = _nothing()
-
-
-def _on(t: torch.Tensor, stream=None):
-    """Context in which work on `t` is queued: its device is the current one
-    and allocations belong to `stream` (the current stream when None)."""
-    if stream is not None:
-        if stream.device != t.device:
-            raise ValueError("stream and tensors are on different devices")
-        return torch.cuda.stream(stream)
-    if t.device.index != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
-    return _NOTHING
-
-
-def _expect(what: str, t: torch.Tensor, dtype, shape, device):
-    """Raise unless t is a contiguous tensor of this type and shape on `device`."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
-
-
-def quantize_tokens(X: torch.Tensor, rows: torch.Tensor | None = None, smooth: torch.Tensor | None = None,
-                    out: QuantizedTokens | None = None, stream=None) -> QuantizedTokens:
-    """INT8 codes of bf16 activations X[T, d_in], one scale per token.
-
-    rows (int32 [R], device): output row r holds token rows[r].  smooth (bf16
-    [d_in]): X / smooth is quantized (awq_scale_activations on the way)."""
-    if X.dtype != torch.bfloat16 or X.dim() != 2 or not X.is_contiguous():
+def _token_operands(X, rows, smooth):
+    """Checked (T, d_in, R) of a quantize_tokens call."""
+    if X.dtype is not torch.bfloat16 or X.dim() != 2 or not X.is_contiguous():
         raise ValueError("X must be a contiguous [T, d_in] bf16 CUDA tensor")
     _require_cuda(X)
     T, d_in = X.shape
@@ -423,29 +417,52 @@ def quantize_tokens(X: torch.Tensor, rows: torch.Tensor | None = None, smooth: t
         _expect("rows", rows, torch.int32, (R,), X.device)
     if smooth is not None:
         _expect("smooth", smooth, torch.bfloat16, (d_in,), X.device)
-    with _on(X, stream):
-        if out is None:
-            out = QuantizedTokens(torch.empty((R, d_in), dtype=torch.int8, device=X.device),
-                                  torch.empty((R,), dtype=torch.float32, device=X.device))
-        else:
-            _expect("out.codes", out.codes, torch.int8, (R, d_in), X.device)
-            _expect("out.scales", out.scales, torch.float32, (R,), X.device)
-        _check(wq_quantize_tokens(X, T, d_in, rows, R, smooth, out.codes, out.scales, stream), "wq_quantize_tokens")
+    return T, d_in, R
+
+
+def quantize_tokens(X: torch.Tensor, rows: torch.Tensor | None = None, smooth: torch.Tensor | None = None,
+                    out: QuantizedTokens | None = None, stream=None) -> QuantizedTokens:
+    """INT8 codes of bf16 activations X[T, d_in], one scale per token.
+
+    rows (int32 [R], device): output row r holds token rows[r].  smooth (bf16
+    [d_in]): X / smooth is quantized (awq_scale_activations on the way)."""
+    T, d_in, R = _token_operands(X, rows, smooth)
+    device = X.device
+    there = _elsewhere(device, stream)
+    if there is not None:
+        with there:
+            return quantize_tokens(X, rows, smooth, out)
+    if out is None:
+        out = QuantizedTokens(torch.empty((R, d_in), dtype=torch.int8, device=device),
+                              torch.empty((R,), dtype=torch.float32, device=device))
+    else:
+        _expect("out.codes", out.codes, torch.int8, (R, d_in), device)
+        _expect("out.scales", out.scales, torch.float32, (R,), device)
+    _check(lib.wq_quantize_tokens(X.data_ptr(), T, d_in, _ptr(rows), R, _ptr(smooth), out.codes.data_ptr(),
+                                  out.scales.data_ptr(), _current_raw_stream(device.index)), "wq_quantize_tokens")
     return out
 
 
-def _w8a8_operands(x, rows, smooth, d_in, device, stream):
-    """The INT8 activations of a product: given, or quantized from bf16."""
+def _w8a8_activations(x, rows, smooth, d_in, device):
+    """(codes pointer, scales pointer, rows, buffer) of a product's INT8
+    activations: given, or quantized from bf16 into a buffer that the caller
+    keeps until the product is queued.  Runs on the current device and stream."""
     if isinstance(x, QuantizedTokens):
         if rows is not None or smooth is not None:
             raise ValueError("rows and smooth apply to bf16 activations; these are quantized already")
         R = x.codes.shape[0]
         _expect("x.codes", x.codes, torch.int8, (R, d_in), device)
         _expect("x.scales", x.scales, torch.float32, (R,), device)
-        return x
-    if x.dim() != 2 or x.shape[1] != d_in or x.device != device:
+        return x.codes.data_ptr(), x.scales.data_ptr(), R, None
+    T, k, R = _token_operands(x, rows, smooth)
+    if k != d_in or x.device != device:
         raise ValueError(f"x must be a contiguous [tokens, {d_in}] bf16 tensor on {device}")
-    return quantize_tokens(x, rows, smooth, stream=stream)
+    buf = torch.empty(R * (d_in + 4), dtype=torch.int8, device=device)  # codes, then scales (d_in is a multiple of 32)
+    codes = buf.data_ptr()
+    scales = codes + R * d_in
+    _check(lib.wq_quantize_tokens(x.data_ptr(), T, d_in, _ptr(rows), R, _ptr(smooth), codes, scales,
+                                  _current_raw_stream(device.index)), "wq_quantize_tokens")
+    return codes, scales, R, buf
 
 
 def _w8a8_output(out, out_dtype, shape, device):
@@ -458,7 +475,7 @@ def _w8a8_output(out, out_dtype, shape, device):
         if out.dtype not in (torch.bfloat16, torch.float32) or (out_dtype or out.dtype) != out.dtype:
             raise ValueError("out must be a bf16 or fp32 tensor (of out_dtype, when both are given)")
         _expect("out", out, out.dtype, shape, device)
-    return out, (WQ_OUT_FP32 if out.dtype == torch.float32 else WQ_OUT_BF16)
+    return out, (WQ_OUT_FP32 if out.dtype is torch.float32 else WQ_OUT_BF16)
 
 
 def linear_w8a8(x, p: PackedLinearW8, out_dtype=None, out: torch.Tensor | None = None,
@@ -469,18 +486,21 @@ def linear_w8a8(x, p: PackedLinearW8, out_dtype=None, out: torch.Tensor | None =
     x: QuantizedTokens, or bf16 activations [M, d_in], which are quantized
     first (smooth as in quantize_tokens).  Layers that share their input
     (q, k and v; gate and up) should quantize it once."""
-    device = p.qweight.device
-    _require_cuda(p.qweight)
-    if p.group_size != p.d_in:
+    qweight, scales, d_out, d_in = p.qweight, p.scales, p.d_out, p.d_in
+    device = qweight.device
+    _require_cuda(qweight)
+    if p.group_size != d_in:
         raise ValueError("linear_w8a8 takes per-channel weights (quantize_w8 without a group_size)")
-    _expect("p.qweight", p.qweight, torch.int32, (p.d_out, p.d_in // 4), device)
-    _expect("p.scales", p.scales, torch.float16, (p.d_out,) if p.scales.dim() == 1 else (p.d_out, 1), device)
-    with _on(p.qweight, stream):
-        x = _w8a8_operands(x, None, smooth, p.d_in, device, stream)
-        M = x.codes.shape[0]
-        out, y_dtype = _w8a8_output(out, out_dtype, (M, p.d_out), device)
-        _check(wq_linear_w8a8(x.codes, x.scales, M, p.qweight, p.scales, p.d_out, p.d_in, out, y_dtype, stream),
-               "wq_linear_w8a8")
+    _expect("p.qweight", qweight, torch.int32, (d_out, d_in // 4), device)
+    _expect("p.scales", scales, torch.float16, (d_out,) if scales.dim() == 1 else (d_out, 1), device)
+    there = _elsewhere(device, stream)
+    if there is not None:
+        with there:
+            return linear_w8a8(x, p, out_dtype, out, smooth)
+    codes, x_scales, M, _buf = _w8a8_activations(x, None, smooth, d_in, device)
+    out, y_dtype = _w8a8_output(out, out_dtype, (M, d_out), device)
+    _check(lib.wq_linear_w8a8(codes, x_scales, M, qweight.data_ptr(), scales.data_ptr(), d_out, d_in, out.data_ptr(),
+                              y_dtype, _current_raw_stream(device.index)), "wq_linear_w8a8")
     return out
 
 
@@ -494,18 +514,21 @@ def linear_w8a8_grouped(x, p: PackedExpertsW8, offsets: torch.Tensor, out_dtype=
     QuantizedTokens with R rows sorted by expert, or bf16 tokens, of which
     rows (int32 [R]) names the one that each row takes.  Rows outside
     [offsets[0], offsets[E]) of the output are not written."""
-    device = p.qweight.device
-    _require_cuda(p.qweight)
-    E = p.experts
-    _expect("p.qweight", p.qweight, torch.int32, (E, p.d_out, p.d_in // 4), device)
-    _expect("p.scales", p.scales, torch.float16, (E, p.d_out), device)
+    qweight, scales, E, d_out, d_in = p.qweight, p.scales, p.experts, p.d_out, p.d_in
+    device = qweight.device
+    _require_cuda(qweight)
+    _expect("p.qweight", qweight, torch.int32, (E, d_out, d_in // 4), device)
+    _expect("p.scales", scales, torch.float16, (E, d_out), device)
     _expect("offsets", offsets, torch.int32, (E + 1,), device)
-    with _on(p.qweight, stream):
-        x = _w8a8_operands(x, rows, smooth, p.d_in, device, stream)
-        R = x.codes.shape[0]
-        out, y_dtype = _w8a8_output(out, out_dtype, (R, p.d_out), device)
-        _check(wq_linear_w8a8_grouped(x.codes, x.scales, R, offsets, E, p.qweight, p.scales, p.d_out, p.d_in, out,
-                                      y_dtype, stream), "wq_linear_w8a8_grouped")
+    there = _elsewhere(device, stream)
+    if there is not None:
+        with there:
+            return linear_w8a8_grouped(x, p, offsets, out_dtype, out, rows, smooth)
+    codes, x_scales, R, _buf = _w8a8_activations(x, rows, smooth, d_in, device)
+    out, y_dtype = _w8a8_output(out, out_dtype, (R, d_out), device)
+    _check(lib.wq_linear_w8a8_grouped(codes, x_scales, R, offsets.data_ptr(), E, qweight.data_ptr(),
+                                      scales.data_ptr(), d_out, d_in, out.data_ptr(), y_dtype,
+                                      _current_raw_stream(device.index)), "wq_linear_w8a8_grouped")
     return out
 
 
