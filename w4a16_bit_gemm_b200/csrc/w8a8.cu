@@ -31,7 +31,10 @@ wq_status run_product(W8A8Args a, void* stream) {
     const wq_status v = device_info(&a.status, &num_sms);
     if (v != WQ_OK) return v;
     if (a.R == 0) return WQ_OK;
-    const cudaError_t e = launch_w8a8_stream(a, num_sms, pdl_enabled(), static_cast<cudaStream_t>(stream));
+    // average rows of an expert that has any
+    const int64_t mean = a.R / (a.E < a.R ? a.E : a.R);
+    const auto launch = mean <= 64 ? launch_w8a8_stream : launch_w8a8_pair;
+    const cudaError_t e = launch(a, num_sms, pdl_enabled(), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? WQ_OK : e == cudaErrorNotSupported ? WQ_ERR_UNSUPPORTED : WQ_ERR_CUDA;
 }
 

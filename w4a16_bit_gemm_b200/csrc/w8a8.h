@@ -37,4 +37,8 @@ struct W8A8Args {
 // cluster when there are few tiles (w8a8_stream.cu).
 cudaError_t launch_w8a8_stream(const W8A8Args& a, int num_sms, bool pdl, cudaStream_t stream);
 
+// Many rows per weight matrix: pairs of CTAs share tiles of 256 channels x up
+// to 256 rows (w8a8_pair.cu).
+cudaError_t launch_w8a8_pair(const W8A8Args& a, int num_sms, bool pdl, cudaStream_t stream);
+
 }  // namespace wq

@@ -1,0 +1,348 @@
+// w8a8_pair.cu -- INT8 x INT8 linear layer, many rows per weight matrix
+// (sm_100a): prefill, long chunks, loaded experts.
+//
+// Y[m, n] = s_m w_n sum_k Xq[m, k] q[n, k] on pairs of SMs: one
+// tcgen05.mma.cta_group::2 (kind::i8, M = 256, K = 32) multiplies 256 output
+// channels, 128 from each CTA's shared memory, with up to 256 rows, half of
+// them from each CTA.  A 1-SM tile of 128 x 256 needs 48 KB of operands per
+// 128 k; a pair needs 32 KB per SM for twice the product, and what bounds this
+// kernel is the stream from L2 into shared memory (about 43 B per clock and SM
+// were sustained by the 1-SM tiles), not the tensor cores.
+//
+// Rows are the N side, so a tile with few rows (the last one of a prompt, a
+// lightly loaded expert) costs its own rows rounded up to 32, not a full tile.
+// The accumulator is int32 in tensor memory, two of 256 columns: the epilogue
+// of a tile runs under the products of the next.  Persistent: each pair walks
+// the tiles in steps of the number of pairs.  Every wait is bounded
+// (WQ_DEVFLAG_TIMEOUT).
+#include <stdint.h>
+
+#include "w8a8.h"
+#include "w8a8_device.cuh"
+#include "wq_kernels.h"
+
+namespace wq {
+namespace {
+
+constexpr int kCh = 256;                 // output channels per tile, 128 per CTA
+constexpr int kKB = 128;                 // k per stage
+constexpr int kMaxRows = 256;            // rows per tile
+constexpr int kATile = 128 * kKB;        // bytes per CTA and stage
+constexpr int kBTile = 128 * kKB;
+constexpr int kStages = 6;
+constexpr int kThreads = 192;            // copy warp, MMA warp, 4 epilogue warps
+constexpr int kTmemCols = 2 * kMaxRows;
+
+struct PairPlan {
+    int step;   // most rows of a tile, a multiple of 32
+    int n_ct;   // channel tiles
+};
+
+// Boxes of 128, 64, 32 and 16 rows: half a tile's rows, a multiple of 16, in as
+// few copies as it has bits.
+struct RowMaps {
+    CUtensorMap m[4];
+};
+
+struct PairBars {
+    uint64_t full[kStages];   // leader: both CTAs' bytes
+    uint64_t empty[kStages];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];    // leader: 4 warps of each CTA
+    uint64_t drain;           // leader
+    uint32_t tmem_slot;
+    int abort_flag;
+};
+
+__host__ __device__ constexpr int table_ints(int E) { return (E + 1 + 3) & ~3; }
+__host__ __device__ constexpr int pair_smem(int E) {
+    return 1024 + kStages * (kATile + kBTile) + 2 * kMaxRows * 4 + 2 * table_ints(E) * 4 + 64 * 4 + (int)sizeof(PairBars);
+}
+static_assert(pair_smem(WQ_INT8_MAX_EXPERTS) <= 227 * 1024, "pair kernel shared memory");
+
+__device__ __forceinline__ void tc_mma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive on this barrier in the CTAs of `mask` once the MMAs issued so far are done.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar, uint16_t mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(mask)
+        : "memory");
+}
+
+// 2-D tiled load into this CTA's shared memory, its bytes counted on a barrier
+// of the pair's leader (cluster_bar).
+__device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const void* tmap, uint32_t cluster_bar, int32_t x,
+                                                 int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(tmap), "r"(cluster_bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
+
+// mbar_wait for a barrier that the other CTA arrives on.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t* status) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        for (int i = 0; i < 16; ++i)
+            if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            raise_flag(status, kFlagTimeout);
+            return false;
+        }
+    }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    w8a8_pair_kernel(const __grid_constant__ RowMaps tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+                     const W8A8Args a, const PairPlan p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* smem_a = smem;
+    uint8_t* smem_b = smem + kStages * kATile;
+    float* row_scale = reinterpret_cast<float*>(smem_b + kStages * kBTile);  // [2][kMaxRows]
+    int* off = reinterpret_cast<int*>(row_scale + 2 * kMaxRows);
+    int* cum = off + table_ints(a.E);
+    int* warp_part = cum + table_ints(a.E);
+    PairBars& bar = *reinterpret_cast<PairBars*>(warp_part + 64);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)(blockIdx.x & 1u);
+    const int worker = (int)(blockIdx.x >> 1), workers = (int)(gridDim.x >> 1);
+    const int nkb = (a.K + kKB - 1) / kKB;
+
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bar.full[s], 1);
+            mbar_init(&bar.empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bar.acc_full[s], 1);
+            mbar_init(&bar.acc_empty[s], 8);
+        }
+        mbar_init(&bar.drain, 1);
+        bar.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar.tmem_slot)),
+                     "r"((uint32_t)kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        tc_fence_before();
+    }
+    pdl_wait_prior();
+    build_tiles(a.offsets, a.E, a.R, p.step, off, cum, warp_part, kThreads, a.status);  // ends with __syncthreads
+    cluster_arrive();
+    cluster_wait();  // both CTAs' barriers are initialised
+    tc_fence_after();
+    const uint32_t tmem_base = bar.tmem_slot;
+    const int total = cum[a.E] * p.n_ct;
+    volatile int* abort_flag = &bar.abort_flag;
+
+    if (warp == 0) {
+        // ---------------- copy warp (both CTAs) ----------------
+        if (lane == 0) {
+            prefetch_tmap(&tmap_w);
+            int it = 0;
+            for (int t = worker; t < total && !*abort_flag; t += workers) {
+                const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
+                const int half = ceil_div(w.n, 32) * 16;  // rows this CTA brings
+                const int wrow = w.e * a.N + w.ct * kCh + rank * 128;
+                const int xrow = w.row0 + rank * half;
+                for (int kb = 0; kb < nkb; ++kb, ++it) {
+                    const int s = it % kStages;
+                    if (it >= kStages && !mbar_wait_cluster(&bar.empty[s], (uint32_t)(it / kStages - 1) & 1u, a.status)) {
+                        atomicExch(&bar.abort_flag, 1);
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], (uint32_t)(2 * (kATile + half * kKB)));
+                    const uint32_t full = map_rank(smem_u32(&bar.full[s]), 0);
+                    tma_load_2d_pair(smem_a + s * kATile, &tmap_w, full, kb * kKB, wrow);
+                    int done = 0;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const int rows = 128 >> b;
+                        if (half & rows) {
+                            tma_load_2d_pair(smem_b + s * kBTile + done * kKB, &tmap_x.m[b], full, kb * kKB, xrow + done);
+                            done += rows;
+                        }
+                    }
+                }
+            }
+            // before the pair ends, the loads in flight (of both CTAs) land in the
+            // leader's count and the leader's last arrivals reach the other CTA
+            for (int j = max(0, it - kStages); j < it; ++j) {
+                const uint32_t parity = (uint32_t)(j / kStages) & 1u;
+                if (rank == 0)
+                    mbar_wait(&bar.full[j % kStages], parity, a.status);
+                else
+                    mbar_wait_cluster(&bar.empty[j % kStages], parity, a.status);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------- MMA warp (leader) ----------------
+        if (rank == 0 && lane == 0) {
+            int it = 0, ti = 0;
+            for (int t = worker; t < total && !*abort_flag; t += workers, ++ti) {
+                const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
+                const uint32_t idesc = mma_idesc_s8(kCh, ceil_div(w.n, 32) * 32);
+                const int acc = ti & 1;
+                bool ok = ti < 2 || mbar_wait_cluster(&bar.acc_empty[acc], (uint32_t)((ti >> 1) - 1) & 1u, a.status);
+                tc_fence_after();
+                for (int kb = 0; ok && kb < nkb; ++kb, ++it) {
+                    const int s = it % kStages;
+                    ok = mbar_wait(&bar.full[s], (uint32_t)(it / kStages) & 1u, a.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a_addr = smem_u32(smem_a + s * kATile), b_addr = smem_u32(smem_b + s * kBTile);
+#pragma unroll
+                    for (int kk = 0; kk < kKB / 32; ++kk)
+                        tc_mma_i8_pair(tmem_base + (uint32_t)(acc * kMaxRows), sw128_kmajor_desc(a_addr + kk * 32),
+                                       sw128_kmajor_desc(b_addr + kk * 32), idesc, (kb | kk) != 0 ? 1u : 0u);
+                    tc_commit_pair(&bar.empty[s], 3);
+                }
+                if (!ok) {
+                    atomicExch(&bar.abort_flag, 1);
+                    break;
+                }
+                tc_commit_pair(&bar.acc_full[acc], 3);
+            }
+            tc_commit_pair(&bar.drain, 1);  // completes once every MMA issued above has
+            mbar_wait(&bar.drain, 0u, a.status);
+        }
+        __syncwarp();
+    } else {
+        // ---------------- epilogue warps (both CTAs) ----------------
+        const int q = warp & 3;            // tensor memory lanes this warp may read
+        const int ch = rank * 128 + q * 32 + lane;
+        const int et = threadIdx.x - 64;   // 0 .. 127
+        int ti = 0;
+        for (int t = worker; t < total; t += workers, ++ti) {
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
+            const int acc = ti & 1;
+            float* rs = row_scale + acc * kMaxRows;
+            for (int i = et; i < w.n; i += 128) rs[i] = a.xs[w.row0 + i];
+            const int c = w.ct * kCh + ch;
+            const bool cv = c < a.N;
+            const float sw = cv ? __half2float(__ushort_as_half(a.ws[(int64_t)w.e * a.N + c])) : 0.0f;
+            named_sync(1, 128);
+            const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bar.acc_full[acc], (uint32_t)(ti >> 1) & 1u, a.status));
+            tc_fence_after();
+            if (!ok) {
+                atomicExch(&bar.abort_flag, 1);
+                break;
+            }
+            const uint32_t dcol = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * kMaxRows);
+            for (int c0 = 0; c0 < w.n; c0 += 32) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(dcol + (uint32_t)c0, v);
+                tc_wait_ld();
+                if (!cv) continue;
+                const int64_t at = (int64_t)(w.row0 + c0) * a.N + c;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (c0 + j < w.n)
+                        w8a8_store(a.Y, a.y_fp32, at + (int64_t)j * a.N, w8a8_value((int)v[j], sw, rs[c0 + j]));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&bar.acc_empty[acc]), 0));
+        }
+        __syncwarp();
+    }
+
+    // ---------------- teardown ----------------
+    // the leader's MMAs read both CTAs' shared memory and arrive on both CTAs'
+    // barriers: neither ends before the other is done
+    tc_fence_before();
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"((uint32_t)kTmemCols)
+                     : "memory");
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_w8a8_pair(const W8A8Args& a, int num_sms, bool pdl, cudaStream_t stream) {
+    PairPlan p = {};
+    p.n_ct = ceil_div(a.N, kCh);
+    const int pairs = num_sms / 2;
+    p.step = kMaxRows;
+    if (!a.offsets) {
+        // rows per tile: the fewest waves' worth of L2 reads (128 bytes per
+        // channel and k block, 64 per row)
+        int64_t best = -1;
+        for (int step = kMaxRows; step >= 32; step -= 32) {
+            const int64_t tiles = (int64_t)ceil_div(a.R, step) * p.n_ct;
+            const int64_t cost = (tiles + pairs - 1) / pairs * (128 * 128 + 64 * step);
+            if (best < 0 || cost < best) {
+                best = cost;
+                p.step = step;
+            }
+        }
+    }
+    const int64_t token_tiles = a.offsets ? (int64_t)(a.E < a.R ? a.E : a.R) + a.R / p.step : ceil_div(a.R, p.step);
+    const int64_t tiles = token_tiles * p.n_ct;
+    if (tiles > 0x7fffffff) return cudaErrorNotSupported;
+
+    RowMaps tx;
+    CUtensorMap tw;
+    CUresult cr = CUDA_SUCCESS;
+    for (int b = 0; b < 4 && cr == CUDA_SUCCESS; ++b)
+        cr = encode_tensor_map_2d(&tx.m[b], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.Xq, (uint64_t)a.K, (uint64_t)a.R,
+                                  (uint64_t)a.K, kKB, 128u >> b, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (cr == CUDA_SUCCESS)
+        cr = encode_tensor_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.qweight, (uint64_t)a.K,
+                                  (uint64_t)a.E * (uint64_t)a.N, (uint64_t)a.K, kKB, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (cr != CUDA_SUCCESS) return cudaErrorInvalidValue;
+    const int smem = pair_smem(a.E);
+    cudaError_t e = cudaFuncSetAttribute(w8a8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, w8a8_pair_kernel, tx, tw, a, p);
+}
+
+}  // namespace wq

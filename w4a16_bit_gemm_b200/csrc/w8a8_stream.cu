@@ -35,7 +35,7 @@ constexpr int kMaxStages = 16;
 constexpr int kMaxSplit = 8;
 
 struct StreamPlan {
-    int nt;       // most rows of a tile (16, 32, 64, 128 or 256)
+    int nt;       // most rows of a tile (16, 32 or 64)
     int box;      // rows of one TMA box of Xq
     int stages;
     int split;    // CTAs that share a tile's K
@@ -303,17 +303,17 @@ cudaError_t launch_w8a8_stream(const W8A8Args& a, int num_sms, bool pdl, cudaStr
     const int per_expert = ceil_div(a.R, a.E < a.R ? a.E : a.R);
     // rows per tile: what an expert holds, with room for an uneven share
     p.nt = 16;
-    while (p.nt < 256 && p.nt < (a.offsets ? 2 * per_expert : per_expert)) p.nt *= 2;
-    p.box = p.nt <= 64 ? 16 : 64;
+    while (p.nt < 64 && p.nt < (a.offsets ? 2 * per_expert : per_expert)) p.nt *= 2;
+    // one matrix: all rows in one box; experts: only boxes that hold rows of theirs
+    p.box = a.offsets ? 16 : p.nt;
     const int64_t token_tiles = a.offsets ? (int64_t)(a.E < a.R ? a.E : a.R) + a.R / p.nt : ceil_div(a.R, p.nt);
     const int64_t tiles = token_tiles * p.n_ct;
     if (tiles > 0x7fffffff) return cudaErrorNotSupported;
     const int nkb = ceil_div(a.K, kKB);
-    const int per_sm = p.nt <= 64 ? 2 : 1;
+    constexpr int per_sm = 2;
     p.split = 1;
-    if (p.nt <= 64)
-        while (p.split < kMaxSplit && tiles * (p.split + 1) <= (int64_t)num_sms * per_sm && nkb >= 2 * (p.split + 1)) ++p.split;
-    const int budget = (per_sm == 2 ? 112 : 225) * 1024 - 1024 - tail_bytes(p.nt, p.split, a.E);
+    while (p.split < kMaxSplit && tiles * (p.split + 1) <= (int64_t)num_sms * per_sm && nkb >= 2 * (p.split + 1)) ++p.split;
+    const int budget = 112 * 1024 - 1024 - tail_bytes(p.nt, p.split, a.E);
     p.stages = budget / (kATile + p.nt * kKB);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     if (p.stages < 2) return cudaErrorInvalidConfiguration;
