@@ -75,7 +75,8 @@ def check_tokens(X, rows=None, smooth=None):
 
 
 # every kernel variant: row lengths on both sides of each thread count, register-held and re-read
-@pytest.mark.parametrize("K", [32, 96, 256, 1024, 1056, 2048, 2080, 4096, 4128, 8192, 8224, 11008, 16384, 16416, 20000])
+@pytest.mark.parametrize("K", [32, 96, 256, 1024, 1056, 2048, 2080, 4096, 4128, 8192, 8224, 11008, 16384, 16416, 20000,
+                               32768, 32800, 65536, 65568, 131040])
 @pytest.mark.parametrize("R", [1, 2, 9])
 def test_tokens_match_definition(K, R):
     check_tokens(activations(R, K, K + R))
@@ -116,7 +117,7 @@ def test_tokens_tiny_huge_and_zero_rows():
     check_tokens(x.to(torch.bfloat16))
 
 
-@pytest.mark.parametrize("K", [64, 1056, 4096, 16416])
+@pytest.mark.parametrize("K", [64, 1056, 4096, 16416, 70016])
 def test_tokens_nonfinite(K):
     x = activations(9, K, 8).float()
     x[1, 3] = float("nan")
@@ -129,7 +130,7 @@ def test_tokens_nonfinite(K):
     check_tokens(x.to(torch.bfloat16))
 
 
-@pytest.mark.parametrize("K", [32, 1056, 4096, 16416])
+@pytest.mark.parametrize("K", [32, 1056, 4096, 16416, 40000, 70016])
 def test_tokens_smoothed_and_gathered(K):
     X = activations(13, K, 9)
     g = torch.Generator().manual_seed(4)
@@ -156,6 +157,22 @@ def test_tokens_smoothing_at_the_ends_of_the_range():
     smooth[2::7] = -3.0
     smooth[3::7] = 2.0 ** -133
     smooth[4::7] = 3e38
+    check_tokens(X.to(torch.bfloat16), smooth=smooth.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("exponent", [-133, -126, -110, -97, -90, -60, 60, 90, 119, 125])
+@pytest.mark.parametrize("K", [64, 70016])
+def test_tokens_smoothing_scales_of_every_size(K, exponent):
+    """Rows and smoothing scales at the borders of what the reciprocal covers."""
+    X = activations(5, K, 14).float()
+    X[1] *= 2.0 ** -90
+    X[2] *= 2.0 ** 90
+    X[3] = 0
+    smooth = torch.rand(K, generator=torch.Generator().manual_seed(2)) + 1
+    check_tokens(X.to(torch.bfloat16), smooth=(smooth * 2.0 ** exponent).to(torch.bfloat16))
+    smooth[5] = smooth[5] * 2.0 ** exponent  # one such channel among ordinary ones
+    check_tokens(X.to(torch.bfloat16), smooth=smooth.to(torch.bfloat16))
+    smooth[6], smooth[7], smooth[8] = 0, float("inf"), float("nan")
     check_tokens(X.to(torch.bfloat16), smooth=smooth.to(torch.bfloat16))
 
 

@@ -6,12 +6,14 @@
 // value, so a row is read once and kept in registers between its maximum and
 // its codes.
 //
-// An IEEE division per value would make the kernel issue-bound (about 10 of
-// the ~16 instructions per value that the copy rate leaves).  t = x * fl(1/s)
-// is within 1.6e-5 of x / s (|t| <= 127.0001, three roundings of 2^-24), and
-// fl32(x / s) within 8e-6, so rint(t) is rint(fl32(x / s)) unless t lies
-// within 1e-4 of a half-integer; only there is the division done.  rint is the
-// addition of 1.5 * 2^23, whose low byte is the code in two's complement.
+// An IEEE division per value would make the kernel issue-bound.  With y =
+// fl32(1/s), q0 = fl32(x y), r = fma(-q0, s, x) and q1 = fma(r, y, q0)
+// (Markstein's correction) rint(q1) = rint(fl32(x / s)): x and the row maximum
+// behind s are bf16, so there are few cases up to a power of two, and
+// tests/token_quotient.c goes through all of them.  (A test for values close
+// to a half-integer with the division done there was tried first: with 8-bit
+// significands exact ties are common, 18.8 instructions per value.)  rint is
+// the addition of 1.5 * 2^23, whose low byte is the code in two's complement.
 #include <stdint.h>
 
 #include "w8a8.h"
@@ -20,7 +22,7 @@
 namespace wq {
 namespace {
 
-constexpr int kTokThreads = 256;
+constexpr int block_threads(int lanes) { return lanes > 256 ? lanes : 256; }  // a row's threads, or several rows'
 constexpr float kRint = 12582912.0f;  // 1.5 * 2^23
 
 __device__ __forceinline__ void unpack8(const uint4& v, float f[8]) {
@@ -32,16 +34,63 @@ __device__ __forceinline__ void unpack8(const uint4& v, float f[8]) {
     }
 }
 
-// bf16_rn(fl32(x / smooth)) for 8 values
-__device__ __forceinline__ uint4 smooth8(const uint4& v, const uint16_t* smooth, int k) {
-    float f[8];
+// 16 bytes of a row, read once.  Not a read-only (.nc) load: with programmatic
+// dependent launch the kernel ahead may write them while this one is resident.
+__device__ __forceinline__ uint4 load_row16(const uint16_t* p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+
+// 8 smoothing scales
+__device__ __forceinline__ uint4 load_smooth(const uint16_t* smooth, int k) {
+    if ((reinterpret_cast<uintptr_t>(smooth) & 15) == 0) return *reinterpret_cast<const uint4*>(smooth + k);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = (uint32_t)smooth[k + 2 * i] | ((uint32_t)smooth[k + 2 * i + 1] << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// bf16_rn(fl32(x / smooth)) for 8 values, with the division.
+__device__ __forceinline__ uint4 smooth8_exact(const uint4& v, const uint4& sm) {
+    float f[8], s[8];
     unpack8(v, f);
+    unpack8(sm, s);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o[i] = bf2_bits(__floats2bfloat162_rn(__fdiv_rn(f[2 * i], s[2 * i]), __fdiv_rn(f[2 * i + 1], s[2 * i + 1])));
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// The same through approximate reciprocals; `largest` takes the largest |smooth|.
+//
+// x and smooth have 8 significant bits, so in the normal range their quotient
+// a / b is never halfway between two bf16 values (that would need a = b m with
+// m odd and of 9 bits, more than 8 bits) and at least 2^-18 of itself away
+// from such a point.  x times the reciprocal is within 2^-22, fl32(x / smooth)
+// within 2^-24: both round to the same bf16.  The row's maximum m tells where
+// this does not hold: beyond 2^120 or NaN a reciprocal or a product may have
+// overflowed (smooth 0, subnormal or NaN among the causes); below 2^-96 values
+// outside the normal range could matter, while under a larger maximum they are
+// coded 0 anyway; a smooth of 2^126 or more has a reciprocal that is flushed
+// to 0.  Such rows are done again with the division.
+__device__ __forceinline__ uint4 smooth8(const uint4& v, const uint4& sm, __nv_bfloat162& largest) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w}, d[4] = {sm.x, sm.y, sm.z, sm.w};
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float s0 = __uint_as_float((uint32_t)__ldg(smooth + k + 2 * i) << 16);
-        const float s1 = __uint_as_float((uint32_t)__ldg(smooth + k + 2 * i + 1) << 16);
-        o[i] = bf2_bits(__floats2bfloat162_rn(__fdiv_rn(f[2 * i], s0), __fdiv_rn(f[2 * i + 1], s1)));
+        float r0, r1;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(__uint_as_float(d[i] << 16)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(__uint_as_float(d[i] & 0xffff0000u)));
+        const float2 t = __fmul2_rn(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)),
+                                    make_float2(r0, r1));
+        o[i] = bf2_bits(__floats2bfloat162_rn(t.x, t.y));
+        largest = __hmax2_nan(largest, __habs2(bits_bf2(d[i])));
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -54,13 +103,31 @@ __device__ __forceinline__ __nv_bfloat162 max8(__nv_bfloat162 m, const uint4& v)
     return m;
 }
 
-// Largest finite |x| of 8 values.
-__device__ __forceinline__ float finite_max8(float m, const uint4& v) {
+// Largest finite |x| of 8 values; bad becomes 1 if one is not finite.
+__device__ __forceinline__ void finite_max8(const uint4& v, float& m, float& bad) {
     float f[8];
     unpack8(v, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (isfinite(f[i])) m = fmaxf(m, fabsf(f[i]));
+    for (int i = 0; i < 8; ++i) {
+        if (isfinite(f[i]))
+            m = fmaxf(m, fabsf(f[i]));
+        else
+            bad = 1.0f;
+    }
+}
+
+// Maximum over the threads of a row (kWarps whole warps; `sub` numbers the
+// block's rows).  All threads of the block call it.
+template <int kWarps>
+__device__ __forceinline__ float row_max(float m, float* part, int sub) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if constexpr (kWarps > 1) {
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, part[sub * kWarps + w]);
+    }
     return m;
 }
 
@@ -76,27 +143,25 @@ __device__ __forceinline__ uint2 codes8_exact(const float f[8], float s) {
     return make_uint2(w[0], w[1]);
 }
 
-// fast: every value of the row is finite and 1/s is a normal number.
+// fast: every value of the row is finite and s >= 2^-96.
 __device__ __forceinline__ uint2 codes8(const uint4& v, float s, float rcp, bool fast) {
-    float f[8];
-    unpack8(v, f);
-    if (fast) {
-        uint32_t m[8];
-        float far = 0.0f;  // largest distance to the nearest integer
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float t = f[i] * rcp;
-            const float r = __fadd_rn(t, kRint);
-            m[i] = __float_as_uint(r);
-            far = fmaxf(far, fabsf(t - __fadd_rn(r, -kRint)));
-        }
-        if (far < 0.4999f) {
-            const uint32_t lo = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
-            const uint32_t hi = __byte_perm(__byte_perm(m[4], m[5], 0x0040), __byte_perm(m[6], m[7], 0x0040), 0x5410);
-            return make_uint2(lo, hi);
-        }
+    if (!fast) {
+        float f[8];
+        unpack8(v, f);
+        return codes8_exact(f, s);
     }
-    return codes8_exact(f, s);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const float2 y = make_float2(rcp, rcp), ns = make_float2(-s, -s), one = make_float2(kRint, kRint);
+    uint32_t m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        const float2 q0 = __fmul2_rn(x, y);
+        const float2 q1 = __ffma2_rn(__ffma2_rn(q0, ns, x), y, q0);
+        const float2 n = __fadd2_rn(q1, one);
+        m[i] = __byte_perm(__float_as_uint(n.x), __float_as_uint(n.y), 0x0040);
+    }
+    return make_uint2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[2], m[3], 0x5410));
 }
 
 struct TokenArgs {
@@ -109,14 +174,13 @@ struct TokenArgs {
     int T, R, K;
 };
 
-// LANES threads per row (32 ... 256), NV 16-byte pieces of the row per thread
+// LANES threads per row (32 ... 1024), NV 16-byte pieces of the row per thread
 // in registers; NV = 0: rows too long for that are read twice.
 template <int LANES, int NV>
-__global__ void __launch_bounds__(kTokThreads) quantize_tokens_kernel(const TokenArgs a) {
-    constexpr int kRows = kTokThreads / LANES, kWarps = LANES / 32;
-    __shared__ float part[kTokThreads / 32];
-    __shared__ float part_finite[kTokThreads / 32];
-    const int l = threadIdx.x % LANES, sub = threadIdx.x / LANES, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(block_threads(LANES)) quantize_tokens_kernel(const TokenArgs a) {
+    constexpr int kThreads = block_threads(LANES), kRows = kThreads / LANES, kWarps = LANES / 32;
+    __shared__ float part[kThreads / 32], part2[kThreads / 32], part3[kThreads / 32];
+    const int l = threadIdx.x % LANES, sub = threadIdx.x / LANES;
     const int r = (int)blockIdx.x * kRows + sub;
     const int pieces = a.K / 8;
     pdl_launch_dependents();
@@ -124,7 +188,7 @@ __global__ void __launch_bounds__(kTokThreads) quantize_tokens_kernel(const Toke
     bool live = r < a.R;
     int src = live ? r : 0;
     if (live && a.rows) {
-        src = __ldg(a.rows + r);
+        src = a.rows[r];
         if (src < 0 || src >= a.T) {
             live = false;
             if (l == 0) raise_flag(a.status, WQ_DEVFLAG_INDEX);
@@ -132,68 +196,68 @@ __global__ void __launch_bounds__(kTokThreads) quantize_tokens_kernel(const Toke
     }
     const uint16_t* x = a.X + (live ? (int64_t)src * a.K : 0);
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    const auto load = [&](int c) {
-        uint4 v = live && c < pieces ? ld_nc_v4(x + 8 * c) : zero;
-        if (a.smooth && live && c < pieces) v = smooth8(v, a.smooth, 8 * c);
-        return v;
+    const bool smoothed = a.smooth && live;
+    __nv_bfloat162 m2 = bits_bf2(0u), largest = bits_bf2(0u);
+    const auto load = [&](int c, bool exact) {
+        if (!live || c >= pieces) return zero;
+        const uint4 v = load_row16(x + 8 * c);
+        if (!smoothed) return v;
+        const uint4 sm = load_smooth(a.smooth, 8 * c);
+        return exact ? smooth8_exact(v, sm) : smooth8(v, sm, largest);
     };
 
     constexpr int kHold = NV > 0 ? NV : 1;
     uint4 held[kHold];
-    __nv_bfloat162 m2 = bits_bf2(0u);
     if constexpr (NV > 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = l + i * LANES;
-            held[i] = live && c < pieces ? ld_nc_v4(x + 8 * c) : zero;
+            held[i] = live && c < pieces ? load_row16(x + 8 * c) : zero;
         }
-        if (a.smooth && live) {
+        if (smoothed) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (l + i * LANES < pieces) held[i] = smooth8(held[i], a.smooth, 8 * (l + i * LANES));
+            for (int i = 0; i < NV; ++i) {
+                const int c = l + i * LANES;
+                if (c < pieces) held[i] = smooth8(held[i], load_smooth(a.smooth, 8 * c), largest);
+            }
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) m2 = max8(m2, held[i]);
     } else {
-        for (int c = l; c < pieces; c += LANES) m2 = max8(m2, load(c));
+        for (int c = l; c < pieces; c += LANES) m2 = max8(m2, load(c, false));
     }
     float amax = __bfloat162float(__hmax_nan(m2.x, m2.y));
-    // a NaN or infinity as +inf, so that the maximum carries it
-    if (!(amax <= 3.4e38f)) amax = __uint_as_float(0x7f800000u);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if constexpr (kWarps > 1) {
-        if ((threadIdx.x & 31) == 0) part[warp] = amax;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, part[sub * kWarps + w]);
-    }
-    const bool finite = amax <= 3.4e38f;
-    if (__syncthreads_or(!finite)) {  // some row of the block holds NaN or infinities: maximum of the others
-        float f = 0.0f;
-        if (!finite) {
+    // NaN, infinities and reciprocals that were flushed to 0 as +inf, so that the maximum carries them
+    if (!(amax <= 3.4e38f) || !(__bfloat162float(__hmax_nan(largest.x, largest.y)) < 8.507059e37f))
+        amax = __uint_as_float(0x7f800000u);
+    amax = row_max<kWarps>(amax, part, sub);
+    const bool sure = amax <= 3.4e38f && (!smoothed || (amax >= 1.26217745e-29f && amax <= 1.32922800e36f));
+    bool finite = true;
+    if (__syncthreads_or(!sure)) {  // rare: some row of the block needs a closer look
+        float f = 0.0f, bad = 0.0f;
+        if (!sure) {
             if constexpr (NV > 0) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i) f = finite_max8(f, held[i]);
+                for (int i = 0; i < NV; ++i) {
+                    if (smoothed) held[i] = load(l + i * LANES, true);
+                    finite_max8(held[i], f, bad);
+                }
             } else {
-                for (int c = l; c < pieces; c += LANES) f = finite_max8(f, load(c));
+                for (int c = l; c < pieces; c += LANES) finite_max8(load(c, true), f, bad);
             }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, o));
-        if ((threadIdx.x & 31) == 0) part_finite[warp] = f;
-        __syncthreads();
-        if (!finite) {
-            amax = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, part_finite[sub * kWarps + w]);
-            if (l == 0) raise_flag(a.status, WQ_DEVFLAG_NONFINITE);
+        f = row_max<kWarps>(f, part2, sub);
+        bad = row_max<kWarps>(bad, part3, sub);
+        if (!sure) {
+            amax = f;
+            finite = bad == 0.0f;
+            if (!finite && l == 0) raise_flag(a.status, WQ_DEVFLAG_NONFINITE);
         }
     }
     float s = __fdiv_rn(amax, 127.0f);
     if (s == 0.0f) s = 1.0f;
     const float rcp = __frcp_rn(s);
-    const bool fast = finite && s >= 7.52316385e-37f;  // 2^-120: 1/s and the products stay normal
+    const bool fast = finite && s >= 1.26217745e-29f;  // 2^-96: the products stay normal
     if (r >= a.R) return;
     if (l == 0) a.x_scales[r] = s;
     uint2* out = reinterpret_cast<uint2*>(a.Xq + (int64_t)r * a.K);
@@ -204,16 +268,16 @@ __global__ void __launch_bounds__(kTokThreads) quantize_tokens_kernel(const Toke
             if (c < pieces) out[c] = codes8(held[i], s, rcp, fast);
         }
     } else {
-        for (int c = l; c < pieces; c += LANES) out[c] = codes8(load(c), s, rcp, fast);
+        for (int c = l; c < pieces; c += LANES) out[c] = codes8(load(c, !sure), s, rcp, fast);
     }
 }
 
 template <int LANES, int NV>
 cudaError_t launch_tokens(const TokenArgs& a, bool pdl, cudaStream_t stream) {
-    constexpr int kRows = kTokThreads / LANES;
+    constexpr int kRows = block_threads(LANES) / LANES;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(((int64_t)a.R + kRows - 1) / kRows));
-    cfg.blockDim = dim3(kTokThreads);
+    cfg.blockDim = dim3(block_threads(LANES));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -246,7 +310,9 @@ cudaError_t launch_quantize_tokens(const void* X, int64_t T, int64_t K, const in
     if (pieces <= 128 * 4) return launch_tokens<128, 4>(a, pdl, stream);
     if (pieces <= 256 * 4) return launch_tokens<256, 4>(a, pdl, stream);
     if (pieces <= 256 * 8) return launch_tokens<256, 8>(a, pdl, stream);
-    return launch_tokens<256, 0>(a, pdl, stream);
+    if (pieces <= 512 * 8) return launch_tokens<512, 8>(a, pdl, stream);
+    if (pieces <= 1024 * 8) return launch_tokens<1024, 8>(a, pdl, stream);
+    return launch_tokens<1024, 0>(a, pdl, stream);
 }
 
 }  // namespace wq

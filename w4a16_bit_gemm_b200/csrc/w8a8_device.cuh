@@ -86,7 +86,7 @@ __device__ __forceinline__ void build_tiles(const int32_t* offsets, int E, int R
     int m = 0;
     bool bad = false;
     for (int i = i0; i < i1; ++i) {
-        const int v = __ldg(offsets + i);
+        const int v = offsets[i];
         const int c = min(max(v, 0), R);
         bad |= v != c || c < m;
         m = max(m, c);
