@@ -166,4 +166,45 @@ __device__ __forceinline__ void w8a8_store(void* Y, int y_fp32, int64_t i, float
         static_cast<__nv_bfloat16*>(Y)[i] = __float2bfloat16_rn(y);
 }
 
+// The first n of COLS columns (rows of the output) of this thread's channel:
+// sums v, row scales rs in shared memory, first output at index `at`.  A warp
+// writes 32 neighbouring channels of a row per column.
+template <int COLS, typename T>
+__device__ __forceinline__ void w8a8_store_typed(T* p, int N, float sw, const float* rs, const uint32_t (&v)[COLS],
+                                                 int n) {
+    if (n >= COLS) {  // no test per column: 75 -> about 10 cycles per column and warp
+        float s[COLS];
+#pragma unroll
+        for (int j = 0; j < COLS; j += 4) *reinterpret_cast<float4*>(s + j) = *reinterpret_cast<const float4*>(rs + j);
+#pragma unroll
+        for (int j = 0; j < COLS; ++j, p += N) {
+            const float y = w8a8_value((int)v[j], sw, s[j]);
+            if constexpr (sizeof(T) == 4)
+                *p = y;
+            else
+                *p = __float2bfloat16_rn(y);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < COLS; ++j, p += N) {
+            if (j < n) {
+                const float y = w8a8_value((int)v[j], sw, rs[j]);
+                if constexpr (sizeof(T) == 4)
+                    *p = y;
+                else
+                    *p = __float2bfloat16_rn(y);
+            }
+        }
+    }
+}
+
+template <int COLS>
+__device__ __forceinline__ void w8a8_store_cols(void* Y, int y_fp32, int64_t at, int N, float sw, const float* rs,
+                                                const uint32_t (&v)[COLS], int n) {
+    if (y_fp32)
+        w8a8_store_typed(static_cast<float*>(Y) + at, N, sw, rs, v, n);
+    else
+        w8a8_store_typed(static_cast<__nv_bfloat16*>(Y) + at, N, sw, rs, v, n);
+}
+
 }  // namespace wq

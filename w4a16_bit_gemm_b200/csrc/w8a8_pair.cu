@@ -25,12 +25,14 @@ namespace wq {
 namespace {
 
 constexpr int kCh = 256;                 // output channels per tile, 128 per CTA
-constexpr int kKB = 128;                 // k per stage
+constexpr int kKB = 128;                 // k per swizzle atom
+constexpr int kAtoms = 2;                // atoms per stage
 constexpr int kMaxRows = 256;            // rows per tile
 constexpr int kATile = 128 * kKB;        // bytes per CTA and stage
 constexpr int kBTile = 128 * kKB;
-constexpr int kStages = 6;
-constexpr int kThreads = 192;            // copy warp, MMA warp, 4 epilogue warps
+constexpr int kStages = 3;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;  // copy warp, MMA warp, epilogue warps
 constexpr int kTmemCols = 2 * kMaxRows;
 
 struct PairPlan {
@@ -48,7 +50,7 @@ struct PairBars {
     uint64_t full[kStages];   // leader: both CTAs' bytes
     uint64_t empty[kStages];
     uint64_t acc_full[2];
-    uint64_t acc_empty[2];    // leader: 4 warps of each CTA
+    uint64_t acc_empty[2];    // leader: the epilogue warps of both CTAs
     uint64_t drain;           // leader
     uint32_t tmem_slot;
     int abort_flag;
@@ -56,7 +58,7 @@ struct PairBars {
 
 __host__ __device__ constexpr int table_ints(int E) { return (E + 1 + 3) & ~3; }
 __host__ __device__ constexpr int pair_smem(int E) {
-    return 1024 + kStages * (kATile + kBTile) + 2 * kMaxRows * 4 + 2 * table_ints(E) * 4 + 64 * 4 + (int)sizeof(PairBars);
+    return 1024 + kStages * kAtoms * (kATile + kBTile) + 2 * kMaxRows * 4 + 2 * table_ints(E) * 4 + 64 * 4 + (int)sizeof(PairBars);
 }
 static_assert(pair_smem(WQ_INT8_MAX_EXPERTS) <= 227 * 1024, "pair kernel shared memory");
 
@@ -125,8 +127,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* smem_a = smem;
-    uint8_t* smem_b = smem + kStages * kATile;
-    float* row_scale = reinterpret_cast<float*>(smem_b + kStages * kBTile);  // [2][kMaxRows]
+    uint8_t* smem_b = smem + kStages * kAtoms * kATile;
+    float* row_scale = reinterpret_cast<float*>(smem_b + kStages * kAtoms * kBTile);  // [2][kMaxRows]
     int* off = reinterpret_cast<int*>(row_scale + 2 * kMaxRows);
     int* cum = off + table_ints(a.E);
     int* warp_part = cum + table_ints(a.E);
@@ -135,7 +137,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)(blockIdx.x & 1u);
     const int worker = (int)(blockIdx.x >> 1), workers = (int)(gridDim.x >> 1);
-    const int nkb = (a.K + kKB - 1) / kKB;
+    const int atoms = (a.K + kKB - 1) / kKB, nkb = (atoms + kAtoms - 1) / kAtoms;
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
@@ -145,7 +147,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar.acc_full[s], 1);
-            mbar_init(&bar.acc_empty[s], 8);
+            mbar_init(&bar.acc_empty[s], 2 * kEpiWarps);
         }
         mbar_init(&bar.drain, 1);
         bar.abort_flag = 0;
@@ -183,16 +185,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         atomicExch(&bar.abort_flag, 1);
                         break;
                     }
-                    if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], (uint32_t)(2 * (kATile + half * kKB)));
+                    const int here = min(kAtoms, atoms - kb * kAtoms);
+                    if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], (uint32_t)(2 * here * (kATile + half * kKB)));
                     const uint32_t full = map_rank(smem_u32(&bar.full[s]), 0);
-                    tma_load_2d_pair(smem_a + s * kATile, &tmap_w, full, kb * kKB, wrow);
-                    int done = 0;
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const int rows = 128 >> b;
-                        if (half & rows) {
-                            tma_load_2d_pair(smem_b + s * kBTile + done * kKB, &tmap_x.m[b], full, kb * kKB, xrow + done);
-                            done += rows;
+                    for (int at = 0; at < kAtoms; ++at) {
+                        if (at >= here) break;
+                        const int x = (kb * kAtoms + at) * kKB;
+                        tma_load_2d_pair(smem_a + (s * kAtoms + at) * kATile, &tmap_w, full, x, wrow);
+                        int done = 0;
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const int rows = 128 >> b;
+                            if (half & rows) {
+                                tma_load_2d_pair(smem_b + (s * kAtoms + at) * kBTile + done * kKB, &tmap_x.m[b], full, x, xrow + done);
+                                done += rows;
+                            }
                         }
                     }
                 }
@@ -223,11 +231,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = mbar_wait(&bar.full[s], (uint32_t)(it / kStages) & 1u, a.status);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(smem_a + s * kATile), b_addr = smem_u32(smem_b + s * kBTile);
+                    const uint64_t ad = sw128_kmajor_desc(smem_u32(smem_a + s * kAtoms * kATile));
+                    const uint64_t bd = sw128_kmajor_desc(smem_u32(smem_b + s * kAtoms * kBTile));
+                    const int here = min(kAtoms, atoms - kb * kAtoms);
 #pragma unroll
-                    for (int kk = 0; kk < kKB / 32; ++kk)
-                        tc_mma_i8_pair(tmem_base + (uint32_t)(acc * kMaxRows), sw128_kmajor_desc(a_addr + kk * 32),
-                                       sw128_kmajor_desc(b_addr + kk * 32), idesc, (kb | kk) != 0 ? 1u : 0u);
+                    for (int at = 0; at < kAtoms; ++at) {
+                        if (at >= here) break;
+#pragma unroll
+                        for (int kk = 0; kk < kKB / 32; ++kk)  // descriptors count 16-byte units
+                            tc_mma_i8_pair(tmem_base + (uint32_t)(acc * kMaxRows), ad + (at * kATile + kk * 32) / 16,
+                                           bd + (at * kBTile + kk * 32) / 16, idesc, (kb | at | kk) != 0 ? 1u : 0u);
+                    }
                     tc_commit_pair(&bar.empty[s], 3);
                 }
                 if (!ok) {
@@ -244,18 +258,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---------------- epilogue warps (both CTAs) ----------------
         const int q = warp & 3;            // tensor memory lanes this warp may read
         const int ch = rank * 128 + q * 32 + lane;
-        const int et = threadIdx.x - 64;   // 0 .. 127
+        const int et = threadIdx.x - 64;
+        const int part = (warp - 2) >> 2;  // which half of the 64-column groups
         int ti = 0;
         for (int t = worker; t < total; t += workers, ++ti) {
             if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
             const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
             const int acc = ti & 1;
             float* rs = row_scale + acc * kMaxRows;
-            for (int i = et; i < w.n; i += 128) rs[i] = a.xs[w.row0 + i];
+            for (int i = et; i < w.n; i += 32 * kEpiWarps) rs[i] = a.xs[w.row0 + i];
             const int c = w.ct * kCh + ch;
             const bool cv = c < a.N;
             const float sw = cv ? __half2float(__ushort_as_half(a.ws[(int64_t)w.e * a.N + c])) : 0.0f;
-            named_sync(1, 128);
+            named_sync(1, 32 * kEpiWarps);
             const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bar.acc_full[acc], (uint32_t)(ti >> 1) & 1u, a.status));
             tc_fence_after();
             if (!ok) {
@@ -263,16 +278,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 break;
             }
             const uint32_t dcol = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * kMaxRows);
-            for (int c0 = 0; c0 < w.n; c0 += 32) {
+            for (int c0 = 32 * part; c0 < w.n; c0 += 64) {
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(dcol + (uint32_t)c0, v);
                 tc_wait_ld();
                 if (!cv) continue;
-                const int64_t at = (int64_t)(w.row0 + c0) * a.N + c;
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (c0 + j < w.n)
-                        w8a8_store(a.Y, a.y_fp32, at + (int64_t)j * a.N, w8a8_value((int)v[j], sw, rs[c0 + j]));
+                w8a8_store_cols(a.Y, a.y_fp32, (int64_t)(w.row0 + c0) * a.N + c, a.N, sw, rs + c0, v, w.n - c0);
             }
             tc_fence_before();
             __syncwarp();
