@@ -3,21 +3,25 @@
 //
 // Y[m, n] = s_m w_n sum_k Xq[m, k] q[n, k].  With few rows the product is bound
 // by the weight stream (one byte per weight), so the weights are the A operand:
-// a tile is 128 output channels x up to NT rows, D[channel][row] int32 in
+// a tile is 128 output channels x up to 64 rows, D[channel][row] int32 in
 // tensor memory, and INT8 needs no dequantization between the two.  TMA brings
-// 128-byte-wide boxes (SWIZZLE_128B, K-major) of weights and rows into a ring,
-// one thread issues tcgen05.mma kind::i8 (M = 128, N = rows rounded up to 16,
-// K = 32), four warps scale and store.  The CUDA cores touch no weight.
+// 128-byte-wide atoms (SWIZZLE_128B, K-major) of weights and rows into a ring,
+// two atoms per stage and instruction, one thread issues tcgen05.mma kind::i8
+// (M = 128, N = rows rounded up to 16, K = 32), four warps scale and store.
+// The CUDA cores touch no weight.
 //
 // Few tiles (one token against 4096 channels has 32) would leave most SMs
-// idle: then a cluster of up to 8 CTAs splits K.  Each CTA owns some of the
-// tile's rows (columns of D); the others send it their int32 partials with
-// st.async, counted on its mbarrier, and it adds them up.  Integer sums do not
-// depend on their order, so the result is the same for every split.
+// idle: then a cluster of up to 8 CTAs splits K.  The columns of D are dealt
+// out to the CTAs in groups of 4; each sends the others their groups of its
+// int32 partials with 16-byte st.async, counted on the receiver's mbarrier,
+// and adds up its own.  Integer sums do not depend on their order, so the
+// result is the same for every split.
 //
 // For one weight matrix, the first weights are requested before the wait for
 // the previous kernel (programmatic dependent launch): they do not depend on
-// it, the activations do.  Every wait is bounded (WQ_DEVFLAG_TIMEOUT).
+// it, the activations do.  What follows the wait is kept short: one load of
+// the rows, the MMAs, one exchange.  Every wait is bounded
+// (WQ_DEVFLAG_TIMEOUT).
 #include <stdint.h>
 
 #include "w8a8.h"
@@ -28,20 +32,26 @@ namespace wq {
 namespace {
 
 constexpr int kCh = 128;                  // output channels per tile (MMA M)
-constexpr int kKB = 128;                  // k per stage (one swizzle atom of bytes)
-constexpr int kATile = kCh * kKB;         // bytes
+constexpr int kAtom = 128;                // k per swizzle atom
+constexpr int kAtoms = 2;                 // atoms per stage
+constexpr int kATile = kCh * kAtom;       // bytes of weights per atom
+constexpr int kMaxRows = 64;              // rows per tile
 constexpr int kThreads = 192;             // copy warp, MMA warp, 4 epilogue warps
-constexpr int kMaxStages = 16;
+constexpr int kMaxStages = 8;
 constexpr int kMaxSplit = 8;
 
 struct StreamPlan {
     int nt;       // most rows of a tile (16, 32 or 64)
-    int box;      // rows of one TMA box of Xq
     int stages;
     int split;    // CTAs that share a tile's K
     int n_ct;     // channel tiles
     int grid;
     int smem;
+};
+
+// Boxes of 16, 32, 48 and 64 rows: a tile's rows rounded up to 16, in one copy.
+struct RowMaps {
+    CUtensorMap m[kMaxRows / 16];
 };
 
 struct StreamBars {
@@ -55,40 +65,42 @@ struct StreamBars {
     int abort_flag;
 };
 
-__host__ __device__ constexpr int align16(int x) { return (x + 15) & ~15; }
-
-// Shared memory behind the stages: partials from the cluster, row scales,
-// tile table, barriers.
-__host__ __device__ constexpr int recv_bytes(int nt, int split) { return split > 1 ? (nt + kMaxSplit) * kCh * 4 : 0; }
+__host__ __device__ constexpr int table_ints(int E) { return (E + 1 + 3) & ~3; }
+// Shared memory behind the stages: partials from the cluster, row scales, tile
+// table, barriers.
+__host__ __device__ constexpr int recv_bytes(int nt, int split) {
+    return split > 1 ? split * ((nt / 4 + split - 1) / split) * kCh * 16 : 0;
+}
 __host__ __device__ constexpr int tail_bytes(int nt, int split, int E) {
-    return recv_bytes(nt, split) + 2 * nt * 4 + align16((E + 1) * 4) * 2 + 64 * 4 + (int)sizeof(StreamBars);
+    return recv_bytes(nt, split) + 2 * nt * 4 + 2 * table_ints(E) * 4 + 64 * 4 + (int)sizeof(StreamBars);
 }
 
-__global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_constant__ CUtensorMap tmap_x,
+__global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_constant__ RowMaps tmap_x,
                                                                const __grid_constant__ CUtensorMap tmap_w,
                                                                const W8A8Args a, const StreamPlan p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const int b_tile = p.nt * kKB;
+    const int b_tile = p.nt * kAtom;
     uint8_t* smem_a = smem;
-    uint8_t* smem_b = smem + p.stages * kATile;
-    uint8_t* tail = smem_b + p.stages * b_tile;
-    uint32_t* recv = reinterpret_cast<uint32_t*>(tail);
+    uint8_t* smem_b = smem + p.stages * kAtoms * kATile;
+    uint8_t* tail = smem_b + p.stages * kAtoms * b_tile;
+    uint4* recv = reinterpret_cast<uint4*>(tail);  // [sender][own group][channel]
     float* row_scale = reinterpret_cast<float*>(tail + recv_bytes(p.nt, p.split));  // [2][nt]
     int* off = reinterpret_cast<int*>(row_scale + 2 * p.nt);
-    int* cum = off + align16((a.E + 1) * 4) / 4;
-    int* warp_part = cum + align16((a.E + 1) * 4) / 4;
+    int* cum = off + table_ints(a.E);
+    int* warp_part = cum + table_ints(a.E);
     StreamBars& bar = *reinterpret_cast<StreamBars*>(warp_part + 64);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)(blockIdx.x % (unsigned)p.split);
     const int worker = (int)(blockIdx.x / (unsigned)p.split), workers = (int)(gridDim.x / (unsigned)p.split);
-    const int nkb = (a.K + kKB - 1) / kKB;
+    const int atoms = (a.K + kAtom - 1) / kAtom, nkb = (atoms + kAtoms - 1) / kAtoms;
     const int kb0 = nkb * rank / p.split, kb1 = nkb * (rank + 1) / p.split;
-    const int tmem_cols = p.nt * 2 < 32 ? 32 : p.nt * 2;
+    const bool whole = a.K % kAtom == 0;  // two atoms per copy
+    const int tmem_cols = p.nt * 2;
 
-    pdl_launch_dependents();
     if (threadIdx.x == 0) {
+        prefetch_tmap(&tmap_w);
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(&bar.full[s], 1);
             mbar_init(&bar.empty[s], 1);
@@ -102,17 +114,11 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
         bar.abort_flag = 0;
         fence_mbar_init();
     }
+    pdl_launch_dependents();
     if (warp == 1) {
         tmem_alloc(&bar.tmem_slot, (uint32_t)tmem_cols);
         tmem_relinquish();
         tc_fence_before();
-    }
-    // one weight matrix: the weights of this CTA's first stages are requested
-    // before anything that depends on the previous kernel
-    int ahead = 0;
-    if (warp == 0 && lane == 0) {
-        prefetch_tmap(&tmap_w);
-        prefetch_tmap(&tmap_x);
     }
     if (a.offsets) pdl_wait_prior();
     build_tiles(a.offsets, a.E, a.R, p.nt, off, cum, warp_part, kThreads, a.status);  // ends with __syncthreads
@@ -125,19 +131,33 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
     if (warp == 0) {
         // ---------------- copy warp ----------------
         if (lane == 0) {
-            int it = 0;
+            int it = 0, ahead = 0;
             bool waited = a.offsets != nullptr;
             for (int t = worker; t < total && !*abort_flag; t += workers) {
                 const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 16);
-                const int boxes = ceil_div(w.n, p.box);
-                const uint32_t bytes = (uint32_t)(kATile + boxes * p.box * kKB);
+                const int rows = (w.n + 15) & ~15;
+                const CUtensorMap* tx = &tmap_x.m[rows / 16 - 1];
                 const int wrow = w.e * a.N + w.ct * kCh;
+                const auto bytes = [&](int kb) {
+                    const int here = whole ? kAtoms : min(kAtoms, atoms - kb * kAtoms);
+                    return (uint32_t)(here * (kATile + rows * kAtom));
+                };
+                const auto load = [&](uint8_t* dst, int atom_bytes, const CUtensorMap* map, uint64_t* full, int kb, int row) {
+                    if (whole) {
+                        tma_load_3d(dst, map, full, 0, row, kb * kAtoms);
+                    } else {
+                        for (int at = 0; at < kAtoms && kb * kAtoms + at < atoms; ++at)
+                            tma_load_3d(dst + at * atom_bytes, map, full, (kb * kAtoms + at) * kAtom, row, 0);
+                    }
+                };
                 if (!waited) {
+                    // one weight matrix: what does not depend on the previous kernel goes first
                     ahead = min(p.stages, kb1 - kb0);
                     for (int i = 0; i < ahead; ++i) {
-                        mbar_arrive_expect_tx(&bar.full[i], bytes);
-                        tma_load_2d(smem_a + i * kATile, &tmap_w, &bar.full[i], (kb0 + i) * kKB, wrow);
+                        mbar_arrive_expect_tx(&bar.full[i], bytes(kb0 + i));
+                        load(smem_a + i * kAtoms * kATile, kATile, &tmap_w, &bar.full[i], kb0 + i, wrow);
                     }
+                    prefetch_tmap(tx);
                     pdl_wait_prior();
                     waited = true;
                 }
@@ -148,12 +168,10 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
                             atomicExch(&bar.abort_flag, 1);
                             break;
                         }
-                        mbar_arrive_expect_tx(&bar.full[s], bytes);
-                        tma_load_2d(smem_a + s * kATile, &tmap_w, &bar.full[s], kb * kKB, wrow);
+                        mbar_arrive_expect_tx(&bar.full[s], bytes(kb));
+                        load(smem_a + s * kAtoms * kATile, kATile, &tmap_w, &bar.full[s], kb, wrow);
                     }
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(smem_b + s * b_tile + b * p.box * kKB, &tmap_x, &bar.full[s], kb * kKB,
-                                    w.row0 + b * p.box);
+                    load(smem_b + s * kAtoms * b_tile, rows * kAtom, tx, &bar.full[s], kb, w.row0);
                 }
             }
             // the loads in flight land before the CTA ends
@@ -167,20 +185,28 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
             int it = 0, ti = 0;
             for (int t = worker; t < total && !*abort_flag; t += workers, ++ti) {
                 const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 16);
-                const uint32_t idesc = mma_idesc_s8(kCh, (w.n + 15) & ~15);
+                const int rows = (w.n + 15) & ~15;
+                const uint32_t idesc = mma_idesc_s8(kCh, rows);
                 const int acc = ti & 1;
                 bool ok = ti < 2 || mbar_wait(&bar.acc_empty[acc], (uint32_t)((ti >> 1) - 1) & 1u, a.status);
                 tc_fence_after();
                 for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
                     const int s = it % p.stages;
+                    const uint64_t ad = sw128_kmajor_desc(smem_u32(smem_a + s * kAtoms * kATile));
+                    const uint64_t bd = sw128_kmajor_desc(smem_u32(smem_b + s * kAtoms * b_tile));
+                    const int here = min(kAtoms, atoms - kb * kAtoms);
                     ok = mbar_wait(&bar.full[s], (uint32_t)(it / p.stages) & 1u, a.status);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(smem_a + s * kATile), b_addr = smem_u32(smem_b + s * b_tile);
 #pragma unroll
-                    for (int kk = 0; kk < kKB / 32; ++kk)
-                        tc_mma_i8(tmem_base + (uint32_t)(acc * p.nt), sw128_kmajor_desc(a_addr + kk * 32),
-                                  sw128_kmajor_desc(b_addr + kk * 32), idesc, (kb != kb0 || kk != 0) ? 1u : 0u);
+                    for (int at = 0; at < kAtoms; ++at) {
+                        if (at >= here) break;
+#pragma unroll
+                        for (int kk = 0; kk < kAtom / 32; ++kk)  // descriptors count 16-byte units
+                            tc_mma_i8(tmem_base + (uint32_t)(acc * p.nt), ad + (at * kATile + kk * 32) / 16,
+                                      bd + (at * rows * kAtom + kk * 32) / 16, idesc,
+                                      (kb != kb0 || at != 0 || kk != 0) ? 1u : 0u);
+                    }
                     tc_commit(&bar.empty[s]);
                 }
                 if (!ok) {
@@ -195,21 +221,33 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
         __syncwarp();
     } else {
         // ---------------- epilogue warps ----------------
-        if (!a.offsets) pdl_wait_prior();
         const int q = warp & 3;            // tensor memory lanes this warp may read
         const int ch = q * 32 + lane;      // channel within the tile
         const int et = threadIdx.x - 64;   // 0 .. 127
-        bool joined = p.split == 1;
+        bool waited = a.offsets != nullptr, joined = p.split == 1;
         int ti = 0;
         for (int t = worker; t < total; t += workers, ++ti) {
             if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
             const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 16);
             const int acc = ti & 1;
-            float* rs = row_scale + acc * p.nt;
-            for (int i = et; i < w.n; i += 128) rs[i] = a.xs[w.row0 + i];
             const int c = w.ct * kCh + ch;
             const bool cv = c < a.N;
             const float sw = cv ? __half2float(__ushort_as_half(a.ws[(int64_t)w.e * a.N + c])) : 0.0f;
+            // groups of 4 columns: group g belongs to CTA g % split of the cluster
+            const int groups = (w.n + 3) >> 2;
+            const int pitch = (groups + p.split - 1) / p.split;  // groups kept per sender
+            const int own = rank < groups ? (groups - rank + p.split - 1) / p.split : 0;
+            if (!joined) {
+                if (et == 0) mbar_arrive_expect_tx(&bar.recv, (uint32_t)((p.split - 1) * own * kCh * 16));
+                cluster_wait();  // the others' barriers are initialised
+                joined = true;
+            }
+            if (!waited) {
+                pdl_wait_prior();
+                waited = true;
+            }
+            float* rs = row_scale + acc * p.nt;
+            if (et < w.n) rs[et] = a.xs[w.row0 + et];
             named_sync(1, 128);
             const bool ok = __all_sync(0xffffffffu, mbar_wait(&bar.acc_full[acc], (uint32_t)(ti >> 1) & 1u, a.status));
             tc_fence_after();
@@ -223,42 +261,29 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
                     uint32_t v[16];
                     tmem_ld_32x32b_x16(dcol + (uint32_t)c0, v);
                     tc_wait_ld();
-                    if (!cv) continue;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c0 + j < w.n)
-                            w8a8_store(a.Y, a.y_fp32, (int64_t)(w.row0 + c0 + j) * a.N + c,
-                                       w8a8_value((int)v[j], sw, rs[c0 + j]));
+                    if (cv)
+                        w8a8_store_cols(a.Y, a.y_fp32, (int64_t)(w.row0 + c0) * a.N + c, a.N, sw, rs + c0, v, w.n - c0);
                 }
             } else {
-                // CTA r of the cluster owns columns [lo(r), lo(r + 1)), lo(r) = ceil(n r / split)
-                const int own0 = (w.n * rank + p.split - 1) / p.split, own1 = (w.n * (rank + 1) + p.split - 1) / p.split;
-                const int pitch = (w.n + p.split - 1) / p.split;  // columns kept per sender
-                if (et == 0) mbar_arrive_expect_tx(&bar.recv, (uint32_t)((p.split - 1) * (own1 - own0) * kCh * 4));
-                if (!joined) {
-                    cluster_wait();  // the others' barriers are initialised
-                    joined = true;
-                }
-                const uint32_t slot = smem_u32(recv) + (uint32_t)((rank * pitch * kCh + ch) * 4);
                 const uint32_t recv_bar = smem_u32(&bar.recv);
-                int r = 0, lo = 0, hi = (w.n + p.split - 1) / p.split;
+                uint32_t slot = smem_u32(recv) + (uint32_t)((rank * pitch * kCh + ch) * 16);
+                int r = 0;
                 for (int c0 = 0; c0 < w.n; c0 += 16) {
                     uint32_t v[16];
                     tmem_ld_32x32b_x16(dcol + (uint32_t)c0, v);
                     tc_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
+                    for (int j = 0; j < 16; j += 4) {
                         if (c0 + j < w.n) {
-                            while (c0 + j >= hi) {
-                                ++r;
-                                lo = hi;
-                                hi = (w.n * (r + 1) + p.split - 1) / p.split;
-                            }
-                            const uint32_t at = slot + (uint32_t)((c0 + j - lo) * kCh * 4);
                             if (r == rank)
-                                recv[(rank * pitch + c0 + j - lo) * kCh + ch] = v[j];
+                                recv[(slot - smem_u32(recv)) / 16] = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
                             else
-                                st_async_b32(map_rank(at, (uint32_t)r), v[j], map_rank(recv_bar, (uint32_t)r));
+                                st_async_v4(map_rank(slot, (uint32_t)r), v[j], v[j + 1], v[j + 2], v[j + 3],
+                                            map_rank(recv_bar, (uint32_t)r));
+                            if (++r == p.split) {
+                                r = 0;
+                                slot += kCh * 16;
+                            }
                         }
                     }
                 }
@@ -266,10 +291,21 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
                     atomicExch(&bar.abort_flag, 1);
                     break;
                 }
-                for (int j = own0; j < own1 && cv; ++j) {
-                    int sum = 0;
-                    for (int s = 0; s < p.split; ++s) sum += (int)recv[(s * pitch + j - own0) * kCh + ch];
-                    w8a8_store(a.Y, a.y_fp32, (int64_t)(w.row0 + j) * a.N + c, w8a8_value(sum, sw, rs[j]));
+                for (int g = 0; g < own; ++g) {
+                    int sum[4] = {0, 0, 0, 0};
+                    for (int s = 0; s < p.split; ++s) {
+                        const uint4 v = recv[(s * pitch + g) * kCh + ch];
+                        sum[0] += (int)v.x;
+                        sum[1] += (int)v.y;
+                        sum[2] += (int)v.z;
+                        sum[3] += (int)v.w;
+                    }
+                    const int col = (g * p.split + rank) * 4;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (cv && col + j < w.n)
+                            w8a8_store(a.Y, a.y_fp32, (int64_t)(w.row0 + col + j) * a.N + c,
+                                       w8a8_value(sum[j], sw, rs[col + j]));
                 }
             }
             tc_fence_before();
@@ -281,14 +317,17 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
     }
 
     // ---------------- teardown ----------------
-    if (p.split > 1) {
-        // no CTA ends while another may still write into its shared memory
-        if (warp < 2) cluster_wait();
-        cluster_arrive();
-        cluster_wait();
-    }
     tc_fence_before();
     __syncthreads();
+    if (p.split > 1) {
+        if (warp < 2) cluster_wait();
+        // All that the others send here has arrived, unless a wait gave up: then
+        // this CTA stays until they have ended or come here too.
+        if (*abort_flag) {
+            cluster_arrive();
+            cluster_wait();
+        }
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, (uint32_t)tmem_cols);
@@ -303,29 +342,30 @@ cudaError_t launch_w8a8_stream(const W8A8Args& a, int num_sms, bool pdl, cudaStr
     const int per_expert = ceil_div(a.R, a.E < a.R ? a.E : a.R);
     // rows per tile: what an expert holds, with room for an uneven share
     p.nt = 16;
-    while (p.nt < 64 && p.nt < (a.offsets ? 2 * per_expert : per_expert)) p.nt *= 2;
-    // one matrix: all rows in one box; experts: only boxes that hold rows of theirs
-    p.box = a.offsets ? 16 : p.nt;
+    while (p.nt < kMaxRows && p.nt < (a.offsets ? 2 * per_expert : per_expert)) p.nt *= 2;
     const int64_t token_tiles = a.offsets ? (int64_t)(a.E < a.R ? a.E : a.R) + a.R / p.nt : ceil_div(a.R, p.nt);
     const int64_t tiles = token_tiles * p.n_ct;
     if (tiles > 0x7fffffff) return cudaErrorNotSupported;
-    const int nkb = ceil_div(a.K, kKB);
+    const int nkb = ceil_div(a.K, kAtom * kAtoms);
     constexpr int per_sm = 2;
     p.split = 1;
-    while (p.split < kMaxSplit && tiles * (p.split + 1) <= (int64_t)num_sms * per_sm && nkb >= 2 * (p.split + 1)) ++p.split;
-    const int budget = 112 * 1024 - 1024 - tail_bytes(p.nt, p.split, a.E);
-    p.stages = budget / (kATile + p.nt * kKB);
+    while (p.split < kMaxSplit && tiles * (p.split + 1) <= (int64_t)num_sms * per_sm && nkb >= p.split + 1) ++p.split;
+    const int tail = 1024 + tail_bytes(p.nt, p.split, a.E);
+    const int stage = kAtoms * (kATile + p.nt * kAtom);
+    p.stages = (112 * 1024 - tail) / stage;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
-    if (p.stages < 2) return cudaErrorInvalidConfiguration;
-    p.smem = 1024 + p.stages * (kATile + p.nt * kKB) + tail_bytes(p.nt, p.split, a.E);
+    if (p.stages < 1) return cudaErrorInvalidConfiguration;
+    p.smem = tail + p.stages * stage;
     p.grid = (int)(p.split > 1 || tiles < (int64_t)num_sms * per_sm ? tiles : (int64_t)num_sms * per_sm) * p.split;
 
-    CUtensorMap tx, tw;
-    CUresult cr = encode_tensor_map_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.Xq, (uint64_t)a.K, (uint64_t)a.R,
-                                       (uint64_t)a.K, kKB, (uint32_t)p.box, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (cr == CUDA_SUCCESS)
-        cr = encode_tensor_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.qweight, (uint64_t)a.K,
-                                  (uint64_t)a.E * (uint64_t)a.N, (uint64_t)a.K, kKB, kCh, CU_TENSOR_MAP_SWIZZLE_128B);
+    RowMaps tx = {};
+    CUtensorMap tw;
+    CUresult cr = encode_tensor_map_k_atoms(&tw, a.qweight, (uint64_t)a.K, (uint64_t)a.E * (uint64_t)a.N, kCh);
+    // one matrix: its tiles' rows are known here, and the last tile's
+    const int tile_rows = ceil_div(ceil_div(a.R, ceil_div(a.R, p.nt)), 16) * 16;
+    for (int rows = 16; rows <= p.nt && cr == CUDA_SUCCESS; rows += 16)
+        if (a.offsets || rows <= tile_rows)
+            cr = encode_tensor_map_k_atoms(&tx.m[rows / 16 - 1], a.Xq, (uint64_t)a.K, (uint64_t)a.R, (uint32_t)rows);
     if (cr != CUDA_SUCCESS) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(w8a8_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;

@@ -151,27 +151,44 @@ bool gemv_kmajor_disabled() {
     return v == 1;
 }
 
+static CUresult encoder_ready() {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!g_encode) {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess || !fn)
+            return CUDA_ERROR_NOT_FOUND;
+        g_encode = reinterpret_cast<EncodeTiledFn>(fn);
+    }
+    return CUDA_SUCCESS;
+}
+
 CUresult encode_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner,
                               uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer,
                               CUtensorMapSwizzle swizzle) {
-    {
-        std::lock_guard<std::mutex> lk(g_mu);
-        if (!g_encode) {
-            void* fn = nullptr;
-            cudaDriverEntryPointQueryResult q;
-            if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
-                    cudaSuccess ||
-                q != cudaDriverEntryPointSuccess || !fn)
-                return CUDA_ERROR_NOT_FOUND;
-            g_encode = reinterpret_cast<EncodeTiledFn>(fn);
-        }
-    }
+    CUresult cr = encoder_ready();
+    if (cr != CUDA_SUCCESS) return cr;
     cuuint64_t dims[2] = {inner, outer};
     cuuint64_t strides[1] = {row_stride_bytes};
     cuuint32_t box[2] = {box_inner, box_outer};
     cuuint32_t estr[2] = {1, 1};
     return g_encode(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+CUresult encode_tensor_map_k_atoms(CUtensorMap* map, const void* base, uint64_t k, uint64_t rows, uint32_t box_rows) {
+    CUresult cr = encoder_ready();
+    if (cr != CUDA_SUCCESS) return cr;
+    const bool whole = k % 128 == 0;
+    cuuint64_t dims[3] = {whole ? 128 : k, rows, whole ? k / 128 : 1};
+    cuuint64_t strides[2] = {k, 128};
+    cuuint32_t box[3] = {128, box_rows, whole ? 2u : 1u};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 wq_status awq_check_args(const void* W_bf16, int64_t d_out, int64_t d_in, const void* X_bf16, int64_t T,
