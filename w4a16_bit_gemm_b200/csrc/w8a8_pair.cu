@@ -40,10 +40,10 @@ struct PairPlan {
     int n_ct;   // channel tiles
 };
 
-// Boxes of 128, 64, 32 and 16 rows: half a tile's rows, a multiple of 16, in as
-// few copies as it has bits.
+// Boxes of 16, 32, ... 128 rows: the half of a tile's rows that a CTA brings, in
+// one copy.
 struct RowMaps {
-    CUtensorMap m[4];
+    CUtensorMap m[8];
 };
 
 struct PairBars {
@@ -80,14 +80,14 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar, uint16_t mask) {
         : "memory");
 }
 
-// 2-D tiled load into this CTA's shared memory, its bytes counted on a barrier
+// 3-D tiled load into this CTA's shared memory, its bytes counted on a barrier
 // of the pair's leader (cluster_bar).
-__device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const void* tmap, uint32_t cluster_bar, int32_t x,
-                                                 int32_t y) {
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const void* tmap, uint32_t cluster_bar, int32_t x,
+                                                 int32_t y, int32_t z) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
-        "l"(tmap), "r"(cluster_bar), "r"(x), "r"(y)
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(tmap), "r"(cluster_bar), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
 
@@ -138,9 +138,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int rank = (int)(blockIdx.x & 1u);
     const int worker = (int)(blockIdx.x >> 1), workers = (int)(gridDim.x >> 1);
     const int atoms = (a.K + kKB - 1) / kKB, nkb = (atoms + kAtoms - 1) / kAtoms;
+    const bool whole = a.K % kKB == 0;  // two atoms per copy
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
+        prefetch_tmap(&tmap_w);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bar.full[s], 1);
             mbar_init(&bar.empty[s], 1);
@@ -172,35 +174,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ---------------- copy warp (both CTAs) ----------------
         if (lane == 0) {
-            prefetch_tmap(&tmap_w);
             int it = 0;
             for (int t = worker; t < total && !*abort_flag; t += workers) {
                 const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
                 const int half = ceil_div(w.n, 32) * 16;  // rows this CTA brings
                 const int wrow = w.e * a.N + w.ct * kCh + rank * 128;
                 const int xrow = w.row0 + rank * half;
+                const CUtensorMap* tx = &tmap_x.m[half / 16 - 1];
                 for (int kb = 0; kb < nkb; ++kb, ++it) {
                     const int s = it % kStages;
                     if (it >= kStages && !mbar_wait_cluster(&bar.empty[s], (uint32_t)(it / kStages - 1) & 1u, a.status)) {
                         atomicExch(&bar.abort_flag, 1);
                         break;
                     }
-                    const int here = min(kAtoms, atoms - kb * kAtoms);
+                    const int here = whole ? kAtoms : min(kAtoms, atoms - kb * kAtoms);
                     if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], (uint32_t)(2 * here * (kATile + half * kKB)));
                     const uint32_t full = map_rank(smem_u32(&bar.full[s]), 0);
-#pragma unroll
-                    for (int at = 0; at < kAtoms; ++at) {
-                        if (at >= here) break;
-                        const int x = (kb * kAtoms + at) * kKB;
-                        tma_load_2d_pair(smem_a + (s * kAtoms + at) * kATile, &tmap_w, full, x, wrow);
-                        int done = 0;
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const int rows = 128 >> b;
-                            if (half & rows) {
-                                tma_load_2d_pair(smem_b + (s * kAtoms + at) * kBTile + done * kKB, &tmap_x.m[b], full, x, xrow + done);
-                                done += rows;
-                            }
+                    uint8_t* as = smem_a + s * kAtoms * kATile;
+                    uint8_t* bs = smem_b + s * kAtoms * kBTile;
+                    if (whole) {
+                        tma_load_3d_pair(as, &tmap_w, full, 0, wrow, kb * kAtoms);
+                        tma_load_3d_pair(bs, tx, full, 0, xrow, kb * kAtoms);
+                    } else {
+                        for (int at = 0; at < here; ++at) {
+                            const int x = (kb * kAtoms + at) * kKB;
+                            tma_load_3d_pair(as + at * kATile, &tmap_w, full, x, wrow, 0);
+                            tma_load_3d_pair(bs + at * half * kKB, tx, full, x, xrow, 0);
                         }
                     }
                 }
@@ -222,7 +221,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int it = 0, ti = 0;
             for (int t = worker; t < total && !*abort_flag; t += workers, ++ti) {
                 const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
-                const uint32_t idesc = mma_idesc_s8(kCh, ceil_div(w.n, 32) * 32);
+                const int half = ceil_div(w.n, 32) * 16;
+                const uint32_t idesc = mma_idesc_s8(kCh, 2 * half);
                 const int acc = ti & 1;
                 bool ok = ti < 2 || mbar_wait_cluster(&bar.acc_empty[acc], (uint32_t)((ti >> 1) - 1) & 1u, a.status);
                 tc_fence_after();
@@ -240,7 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < kKB / 32; ++kk)  // descriptors count 16-byte units
                             tc_mma_i8_pair(tmem_base + (uint32_t)(acc * kMaxRows), ad + (at * kATile + kk * 32) / 16,
-                                           bd + (at * kBTile + kk * 32) / 16, idesc, (kb | at | kk) != 0 ? 1u : 0u);
+                                           bd + (at * half * kKB + kk * 32) / 16, idesc, (kb | at | kk) != 0 ? 1u : 0u);
                     }
                     tc_commit_pair(&bar.empty[s], 3);
                 }
@@ -330,15 +330,14 @@ cudaError_t launch_w8a8_pair(const W8A8Args& a, int num_sms, bool pdl, cudaStrea
     const int64_t tiles = token_tiles * p.n_ct;
     if (tiles > 0x7fffffff) return cudaErrorNotSupported;
 
-    RowMaps tx;
+    RowMaps tx = {};
     CUtensorMap tw;
-    CUresult cr = CUDA_SUCCESS;
-    for (int b = 0; b < 4 && cr == CUDA_SUCCESS; ++b)
-        cr = encode_tensor_map_2d(&tx.m[b], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.Xq, (uint64_t)a.K, (uint64_t)a.R,
-                                  (uint64_t)a.K, kKB, 128u >> b, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (cr == CUDA_SUCCESS)
-        cr = encode_tensor_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.qweight, (uint64_t)a.K,
-                                  (uint64_t)a.E * (uint64_t)a.N, (uint64_t)a.K, kKB, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    CUresult cr = encode_tensor_map_k_atoms(&tw, a.qweight, (uint64_t)a.K, (uint64_t)a.E * (uint64_t)a.N, 128);
+    // one matrix: no tile has more rows than the first
+    const int most = ceil_div(ceil_div(a.R, ceil_div(a.R, p.step)), 32) * 16;
+    for (int half = 16; half <= p.step / 2 && cr == CUDA_SUCCESS; half += 16)
+        if (a.offsets || half <= most)
+            cr = encode_tensor_map_k_atoms(&tx.m[half / 16 - 1], a.Xq, (uint64_t)a.K, (uint64_t)a.R, (uint32_t)half);
     if (cr != CUDA_SUCCESS) return cudaErrorInvalidValue;
     const int smem = pair_smem(a.E);
     cudaError_t e = cudaFuncSetAttribute(w8a8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
