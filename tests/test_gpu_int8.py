@@ -256,6 +256,47 @@ def test_linear_whole_path_from_bf16():
     assert torch.equal(one, two)
 
 
+def check_linear_bf16(M, N, K, seed=0, dtype=torch.bfloat16, smooth=False, X=None):
+    """bf16 activations in one call, quantized inside the product or ahead of it."""
+    b = _b()
+    X = activations(M, K, seed) if X is None else X
+    sm = (torch.rand(K, generator=torch.Generator().manual_seed(seed)) + 0.2).to(torch.bfloat16) if smooth else None
+    _, _, wq, ws = operands(1, N, K, seed)
+    xq, xs, bad = ref.quantize_tokens(ref.smoothed(X, sm) if smooth else X)
+    y, y64 = ref.product(xq, xs, wq, ws)
+    got = b.linear_w8a8(X.cuda(), dense(wq, ws), out_dtype=dtype, smooth=sm.cuda() if smooth else None)
+    ref.check(got, y, y64)
+    _, flags = b.device_error()
+    assert flags == (b.WQ_DEVFLAG_NONFINITE if bad else 0)
+
+
+@pytest.mark.parametrize("smooth", [False, True])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 7, 8, 9, 13, 16, 17, 80])
+@pytest.mark.parametrize("N,K", [(1, 32), (130, 96), (128, 128), (300, 288), (1000, 1056), (520, 4096), (2050, 2080)])
+def test_linear_from_bf16(M, N, K, smooth):
+    check_linear_bf16(M, N, K, M + N + K, torch.float32 if (M + N) % 2 else torch.bfloat16, smooth)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (16, 4096, 11008), (5, 4096, 11008), (16, 11008, 4096),
+                                   (2, 28672, 1024), (16, 128, 20480), (9, 300, 40000), (1, 130, 131040)])
+def test_linear_from_bf16_decode_shapes(M, N, K):
+    check_linear_bf16(M, N, K, 5)
+    check_linear_bf16(M, N, K, 6, torch.float32, True)
+
+
+@pytest.mark.parametrize("M,N,K", [(6, 300, 1056), (16, 4096, 512), (40, 200, 512)])
+def test_linear_from_bf16_odd_values(M, N, K):
+    x = activations(M, K, 3).float()
+    x[0] = 0
+    x[1, 5] = float("nan")
+    x[2, K - 1] = float("inf")
+    x[2, 3] = -float("inf")
+    x[3] *= 2.0 ** -126
+    x[4] = float("nan")
+    x[5, : K // 2] = 0
+    check_linear_bf16(M, N, K, X=x.to(torch.bfloat16))
+
+
 def test_linear_no_tokens():
     b = _b()
     _, _, wq, ws = operands(1, 40, 64, 0)
@@ -323,6 +364,49 @@ def test_grouped_bad_offsets_are_flagged_and_stay_in_bounds(offsets):
     st, flags = b.device_error()
     assert st == b.WQ_ERR_INVALID_ARG and flags == b.WQ_DEVFLAG_INDEX
     ref.check(got, y, y64)
+
+
+def check_grouped_bf16(counts, N, K, T, seed=0, dtype=torch.bfloat16, smooth=False, behind=0, bad_rows=False):
+    b = _b()
+    E, R = len(counts), sum(counts) + behind
+    g = torch.Generator().manual_seed(seed)
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    X = activations(T, K, seed)
+    rows = torch.randint(0, T, (R,), generator=g).to(torch.int32)
+    dead = torch.zeros(R, dtype=torch.bool)
+    if bad_rows:
+        rows[1::5], dead[1::5] = T, True
+        rows[2::7], dead[2::7] = -3, True
+    sm = (torch.rand(K, generator=g) + 0.2).to(torch.bfloat16) if smooth else None
+    _, _, wq, ws = operands(1, N, K, seed, E)
+    x = X[rows.clamp(0, T - 1).long()]
+    xq, xs, _ = ref.quantize_tokens(ref.smoothed(x, sm) if smooth else x)
+    xq[dead.numpy()], xs[dead.numpy()] = 0, 1
+    held = torch.randn(R, N, generator=g).to(dtype)
+    y, y64 = ref.grouped(xq, xs, wq, ws, offsets, held)
+    out = b.linear_w8a8_grouped(X.cuda(), experts(wq, ws), torch.from_numpy(offsets.astype(np.int32)).cuda(),
+                                out=held.cuda(), rows=rows.cuda(), smooth=sm.cuda() if smooth else None)
+    ref.check(out, y, y64)
+    _, flags = b.device_error()
+    assert flags == (b.WQ_DEVFLAG_INDEX if bad_rows else 0)
+
+
+@pytest.mark.parametrize("counts", [[1, 1], [0, 2, 0], [8], [9, 0, 1], [16, 0, 3], [17, 2], [40], [0, 0, 5, 1, 1],
+                                    [1] * 20, [3] * 60, [200, 30]], ids=lambda c: "-".join(map(str, c))[:24])
+@pytest.mark.parametrize("N,K", [(70, 96), (257, 1056), (520, 2048)])
+def test_grouped_from_bf16(counts, N, K):
+    check_grouped_bf16(counts, N, K, 7, len(counts) + N)
+    check_grouped_bf16(counts, N, K, 50, len(counts) + K, torch.float32, True, behind=3)
+
+
+def test_grouped_from_bf16_one_user():
+    check_grouped_bf16([0, 1, 0, 0, 0, 1, 0, 0], 11008, 512, 1, 1)
+    check_grouped_bf16([0, 1, 0, 0, 0, 1, 0, 0], 2048, 4096, 1, 2, smooth=True)
+
+
+@pytest.mark.parametrize("counts", [[5, 0, 6], [100, 120]])
+def test_grouped_from_bf16_bad_rows(counts):
+    check_grouped_bf16(counts, 200, 288, 6, 3, torch.float32, bad_rows=True)
 
 
 def test_grouped_equals_dense_per_expert():

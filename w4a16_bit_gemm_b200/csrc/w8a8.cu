@@ -15,27 +15,101 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 bool depth_ok(int64_t d_in) { return d_in >= 32 && d_in % 32 == 0 && d_in <= WQ_INT8_MAX_D_IN; }
 
-// `rows` of activations and outputs; their arrays may be NULL when there are none.
-wq_status check_product(const int8_t* Xq, const float* x_scales, int64_t rows, const uint32_t* qweight,
-                        const void* scales, int64_t d_out, int64_t d_in, const void* Y, int32_t y_dtype) {
+// `rows` of outputs; arrays that belong to them may be NULL when there are none.
+wq_status check_product(int64_t rows, const uint32_t* qweight, const void* scales, int64_t d_out, int64_t d_in,
+                        const void* Y, int32_t y_dtype) {
     if (rows < 0 || rows > kMaxInt32 || d_out < 1 || d_out > kMaxInt32 || !depth_ok(d_in)) return WQ_ERR_INVALID_ARG;
     if (y_dtype != WQ_OUT_BF16 && y_dtype != WQ_OUT_FP32) return WQ_ERR_INVALID_ARG;
     if (!qweight || !scales || !aligned(qweight, 16) || !aligned(scales, 2)) return WQ_ERR_INVALID_ARG;
-    if (rows > 0 && (!Xq || !x_scales || !Y)) return WQ_ERR_INVALID_ARG;
-    if (!aligned(Xq, 16) || !aligned(x_scales, 4) || !aligned(Y, 16)) return WQ_ERR_INVALID_ARG;
+    if ((rows > 0 && !Y) || !aligned(Y, 16)) return WQ_ERR_INVALID_ARG;
     return WQ_OK;
 }
 
-wq_status run_product(W8A8Args a, void* stream) {
+wq_status check_codes(const int8_t* Xq, const float* x_scales, int64_t rows) {
+    if (rows > 0 && (!Xq || !x_scales)) return WQ_ERR_INVALID_ARG;
+    return aligned(Xq, 16) && aligned(x_scales, 4) ? WQ_OK : WQ_ERR_INVALID_ARG;
+}
+
+wq_status check_tokens(const void* X, int64_t T, int64_t d_in, const int32_t* rows, int64_t R, const void* smooth) {
+    if (T < 0 || T > kMaxInt32 || R < 0 || R > kMaxInt32 || !depth_ok(d_in)) return WQ_ERR_INVALID_ARG;
+    if (!rows && R != T) return WQ_ERR_INVALID_ARG;
+    if (R > 0 && T > 0 && !X) return WQ_ERR_INVALID_ARG;
+    return aligned(X, 16) && aligned(rows, 4) && aligned(smooth, 2) ? WQ_OK : WQ_ERR_INVALID_ARG;
+}
+
+wq_status check_experts(const int32_t* offsets, int64_t E, int64_t d_out) {
+    if (!offsets || !aligned(offsets, 4) || E < 1) return WQ_ERR_INVALID_ARG;
+    if (E > WQ_INT8_MAX_EXPERTS) return WQ_ERR_UNSUPPORTED;
+    return E * d_out <= kMaxInt32 ? WQ_OK : WQ_ERR_INVALID_ARG;
+}
+
+W8A8Args product_args(int64_t R, const int32_t* offsets, int64_t E, const uint32_t* qweight, const void* scales,
+                      int64_t d_out, int64_t d_in, void* Y, int32_t y_dtype) {
+    W8A8Args a = {};
+    a.offsets = offsets;
+    a.qweight = qweight;
+    a.ws = static_cast<const uint16_t*>(scales);
+    a.Y = Y;
+    a.R = (int)R;
+    a.N = (int)d_out;
+    a.K = (int)d_in;
+    a.E = (int)E;
+    a.y_fp32 = y_dtype == WQ_OUT_FP32;
+    return a;
+}
+
+wq_status status_of(cudaError_t e) {
+    return e == cudaSuccess ? WQ_OK : e == cudaErrorNotSupported ? WQ_ERR_UNSUPPORTED : WQ_ERR_CUDA;
+}
+
+// The product of quantized rows: up to 64 rows per matrix (on average over the
+// experts that can have any) stream the weights, more share tiles between two
+// SMs.  Measured on both sides: see the kernels.
+cudaError_t run_product(const W8A8Args& a, int num_sms, cudaStream_t stream) {
+    const int mean = a.R / (a.E < a.R ? a.E : a.R);
+    return mean <= 64 ? launch_w8a8_stream(a, pdl_enabled(), stream) : launch_w8a8_pair(a, num_sms, pdl_enabled(), stream);
+}
+
+wq_status product_of_codes(W8A8Args a, const int8_t* Xq, const float* x_scales, void* stream) {
     int num_sms = 0;
     const wq_status v = device_info(&a.status, &num_sms);
     if (v != WQ_OK) return v;
     if (a.R == 0) return WQ_OK;
-    // average rows of an expert that has any
-    const int64_t mean = a.R / (a.E < a.R ? a.E : a.R);
-    const auto launch = mean <= 64 ? launch_w8a8_stream : launch_w8a8_pair;
-    const cudaError_t e = launch(a, num_sms, pdl_enabled(), static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? WQ_OK : e == cudaErrorNotSupported ? WQ_ERR_UNSUPPORTED : WQ_ERR_CUDA;
+    a.Xq = Xq;
+    a.xs = x_scales;
+    return status_of(run_product(a, num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+// bf16 rows: quantized inside the product where that fits, else into the
+// workspace (codes, then scales).
+wq_status product_of_bf16(W8A8Args a, const void* X, int64_t T, const int32_t* rows, const void* smooth, void* workspace,
+                          size_t workspace_bytes, size_t needed, void* stream) {
+    if (workspace_bytes < needed || (needed > 0 && (!workspace || !aligned(workspace, 16)))) return WQ_ERR_INVALID_ARG;
+    int num_sms = 0;
+    const wq_status v = device_info(&a.status, &num_sms);
+    if (v != WQ_OK) return v;
+    if (a.R == 0) return WQ_OK;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (needed == 0) {
+        a.X = static_cast<const uint16_t*>(X);
+        a.rows = rows;
+        a.smooth = static_cast<const uint16_t*>(smooth);
+        a.T = (int)T;
+        return status_of(launch_w8a8_rows(a, pdl_enabled(), s));
+    }
+    int8_t* codes = static_cast<int8_t*>(workspace);
+    float* scales = reinterpret_cast<float*>(codes + (int64_t)a.R * a.K);
+    const cudaError_t e = launch_quantize_tokens(X, T, a.K, rows, a.R, smooth, codes, scales, a.status, pdl_enabled(), s);
+    if (e != cudaSuccess) return WQ_ERR_CUDA;
+    a.Xq = codes;
+    a.xs = scales;
+    return status_of(run_product(a, num_sms, s));
+}
+
+size_t bf16_workspace(int64_t R, int64_t E, bool grouped, int64_t d_out, int64_t d_in) {
+    if (R < 1 || R > kMaxInt32 || E < 1 || E > WQ_INT8_MAX_EXPERTS || d_out < 1 || d_out > kMaxInt32 || !depth_ok(d_in))
+        return 0;
+    return w8a8_rows_fit(R, E, grouped, d_out, d_in) ? 0 : (size_t)(R * (d_in + 4));
 }
 
 }  // namespace
@@ -44,15 +118,12 @@ extern "C" {
 
 wq_status wq_quantize_tokens(const void* X_bf16, int64_t T, int64_t d_in, const int32_t* rows, int64_t R,
                              const void* smooth_bf16, int8_t* Xq, float* x_scales, void* stream) {
-    if (T < 0 || T > kMaxInt32 || R < 0 || R > kMaxInt32 || !depth_ok(d_in)) return WQ_ERR_INVALID_ARG;
-    if (!rows && R != T) return WQ_ERR_INVALID_ARG;
-    if (R > 0 && (!Xq || !x_scales || (T > 0 && !X_bf16))) return WQ_ERR_INVALID_ARG;
-    if (!aligned(X_bf16, 16) || !aligned(Xq, 16) || !aligned(x_scales, 4) || !aligned(rows, 4) ||
-        !aligned(smooth_bf16, 2))
-        return WQ_ERR_INVALID_ARG;
+    wq_status v = check_tokens(X_bf16, T, d_in, rows, R, smooth_bf16);
+    if (v == WQ_OK) v = check_codes(Xq, x_scales, R);
+    if (v != WQ_OK) return v;
     uint32_t* status = nullptr;
     int num_sms = 0;
-    const wq_status v = device_info(&status, &num_sms);
+    v = device_info(&status, &num_sms);
     if (v != WQ_OK) return v;
     if (R == 0) return WQ_OK;
     const cudaError_t e = launch_quantize_tokens(X_bf16, T, d_in, rows, R, smooth_bf16, Xq, x_scales, status,
@@ -63,43 +134,55 @@ wq_status wq_quantize_tokens(const void* X_bf16, int64_t T, int64_t d_in, const 
 wq_status wq_linear_w8a8(const int8_t* Xq, const float* x_scales, int64_t M, const uint32_t* qweight,
                          const void* scales_fp16, int64_t d_out, int64_t d_in, void* Y, int32_t y_dtype,
                          void* stream) {
-    const wq_status v = check_product(Xq, x_scales, M, qweight, scales_fp16, d_out, d_in, Y, y_dtype);
+    wq_status v = check_product(M, qweight, scales_fp16, d_out, d_in, Y, y_dtype);
+    if (v == WQ_OK) v = check_codes(Xq, x_scales, M);
     if (v != WQ_OK) return v;
-    W8A8Args a = {};
-    a.Xq = Xq;
-    a.xs = x_scales;
-    a.qweight = qweight;
-    a.ws = static_cast<const uint16_t*>(scales_fp16);
-    a.Y = Y;
-    a.R = (int)M;
-    a.N = (int)d_out;
-    a.K = (int)d_in;
-    a.E = 1;
-    a.y_fp32 = y_dtype == WQ_OUT_FP32;
-    return run_product(a, stream);
+    return product_of_codes(product_args(M, nullptr, 1, qweight, scales_fp16, d_out, d_in, Y, y_dtype), Xq, x_scales,
+                            stream);
 }
 
 wq_status wq_linear_w8a8_grouped(const int8_t* Xq, const float* x_scales, int64_t R, const int32_t* offsets, int64_t E,
                                  const uint32_t* qweight, const void* scales_fp16, int64_t d_out, int64_t d_in,
                                  void* Y, int32_t y_dtype, void* stream) {
-    const wq_status v = check_product(Xq, x_scales, R, qweight, scales_fp16, d_out, d_in, Y, y_dtype);
+    wq_status v = check_product(R, qweight, scales_fp16, d_out, d_in, Y, y_dtype);
+    if (v == WQ_OK) v = check_codes(Xq, x_scales, R);
+    if (v == WQ_OK) v = check_experts(offsets, E, d_out);
     if (v != WQ_OK) return v;
-    if (!offsets || !aligned(offsets, 4) || E < 1) return WQ_ERR_INVALID_ARG;
-    if (E > WQ_INT8_MAX_EXPERTS) return WQ_ERR_UNSUPPORTED;
-    if (E * d_out > kMaxInt32) return WQ_ERR_INVALID_ARG;
-    W8A8Args a = {};
-    a.Xq = Xq;
-    a.xs = x_scales;
-    a.offsets = offsets;
-    a.qweight = qweight;
-    a.ws = static_cast<const uint16_t*>(scales_fp16);
-    a.Y = Y;
-    a.R = (int)R;
-    a.N = (int)d_out;
-    a.K = (int)d_in;
-    a.E = (int)E;
-    a.y_fp32 = y_dtype == WQ_OUT_FP32;
-    return run_product(a, stream);
+    return product_of_codes(product_args(R, offsets, E, qweight, scales_fp16, d_out, d_in, Y, y_dtype), Xq, x_scales,
+                            stream);
+}
+
+size_t wq_linear_w8a8_bf16_workspace_bytes(int64_t M, int64_t d_out, int64_t d_in) {
+    return bf16_workspace(M, 1, false, d_out, d_in);
+}
+
+size_t wq_linear_w8a8_grouped_bf16_workspace_bytes(int64_t R, int64_t E, int64_t d_out, int64_t d_in) {
+    return bf16_workspace(R, E, true, d_out, d_in);
+}
+
+wq_status wq_linear_w8a8_bf16(const void* X_bf16, int64_t M, const void* smooth_bf16, const uint32_t* qweight,
+                              const void* scales_fp16, int64_t d_out, int64_t d_in, void* Y, int32_t y_dtype,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+    wq_status v = check_product(M, qweight, scales_fp16, d_out, d_in, Y, y_dtype);
+    if (v == WQ_OK) v = check_tokens(X_bf16, M, d_in, nullptr, M, smooth_bf16);
+    if (v != WQ_OK) return v;
+    return product_of_bf16(product_args(M, nullptr, 1, qweight, scales_fp16, d_out, d_in, Y, y_dtype), X_bf16, M,
+                           nullptr, smooth_bf16, workspace, workspace_bytes,
+                           wq_linear_w8a8_bf16_workspace_bytes(M, d_out, d_in), stream);
+}
+
+wq_status wq_linear_w8a8_grouped_bf16(const void* X_bf16, int64_t T, const int32_t* rows, int64_t R,
+                                      const void* smooth_bf16, const int32_t* offsets, int64_t E,
+                                      const uint32_t* qweight, const void* scales_fp16, int64_t d_out, int64_t d_in,
+                                      void* Y, int32_t y_dtype, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+    wq_status v = check_product(R, qweight, scales_fp16, d_out, d_in, Y, y_dtype);
+    if (v == WQ_OK) v = check_tokens(X_bf16, T, d_in, rows, R, smooth_bf16);
+    if (v == WQ_OK) v = check_experts(offsets, E, d_out);
+    if (v != WQ_OK) return v;
+    return product_of_bf16(product_args(R, offsets, E, qweight, scales_fp16, d_out, d_in, Y, y_dtype), X_bf16, T, rows,
+                           smooth_bf16, workspace, workspace_bytes,
+                           wq_linear_w8a8_grouped_bf16_workspace_bytes(R, E, d_out, d_in), stream);
 }
 
 }  // extern "C"

@@ -18,13 +18,23 @@ __host__ __device__ constexpr uint32_t mma_idesc_s8(int M, int N) {
     return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void tc_mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+__device__ __forceinline__ void tc_mma_i8(bool one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                           uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"((int)one)
         : "memory");
+}
+
+// One lane of a converged warp.  The copy and MMA warps run their loops as whole
+// warps and let this lane's predicate pick the thread that issues: addresses and
+// descriptors then stay in uniform registers (a loop inside "if (lane == 0)"
+// took 90 to 135 cycles per MMA and about 200 per copy).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
 }
 
 // ------------------------------------------------------------------------
@@ -41,7 +51,12 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t smem_addr, uint32_t rank) 
     return r;
 }
 
-// 16-byte store into another CTA's shared memory, counted on its mbarrier.
+// 4- and 16-byte stores into another CTA's shared memory, counted on its mbarrier.
+__device__ __forceinline__ void st_async_b32(uint32_t cluster_addr, uint32_t v, uint32_t cluster_bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr),
+                 "r"(v), "r"(cluster_bar)
+                 : "memory");
+}
 __device__ __forceinline__ void st_async_v4(uint32_t cluster_addr, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3,
                                             uint32_t cluster_bar) {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
@@ -51,13 +66,27 @@ __device__ __forceinline__ void st_async_v4(uint32_t cluster_addr, uint32_t v0, 
 }
 
 // 3-D tiled load global -> shared, completion counted on `bar` (bytes).
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* tmap, uint64_t* bar, int32_t x, int32_t y,
-                                            int32_t z) {
+__device__ __forceinline__ void tma_load_3d(bool one, uint32_t smem_dst, const void* tmap, uint32_t bar, int32_t x,
+                                            int32_t y, int32_t z) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
-        "[%2];" ::"r"(smem_u32(smem_dst)),
-        "l"(tmap), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];\n\t}" ::"r"(smem_dst),
+        "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z), "r"((int)one)
         : "memory");
+}
+
+// named_sync that tells every thread whether `go` held in all of them: warps
+// that may have given up at different times leave a loop together.
+__device__ __forceinline__ bool named_sync_and(int id, int nthreads, bool go) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
+        "bar.red.and.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(all)
+        : "r"(id), "r"(nthreads), "r"((uint32_t)go)
+        : "memory");
+    return all != 0;
 }
 
 // ------------------------------------------------------------------------

@@ -62,12 +62,12 @@ __host__ __device__ constexpr int pair_smem(int E) {
 }
 static_assert(pair_smem(WQ_INT8_MAX_EXPERTS) <= 227 * 1024, "pair kernel shared memory");
 
-__device__ __forceinline__ void tc_mma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+__device__ __forceinline__ void tc_mma_i8_pair(bool one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"((int)one)
         : "memory");
 }
 
@@ -82,12 +82,13 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar, uint16_t mask) {
 
 // 3-D tiled load into this CTA's shared memory, its bytes counted on a barrier
 // of the pair's leader (cluster_bar).
-__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const void* tmap, uint32_t cluster_bar, int32_t x,
-                                                 int32_t y, int32_t z) {
+__device__ __forceinline__ void tma_load_3d_pair(bool one, uint32_t smem_dst, const void* tmap, uint32_t cluster_bar,
+                                                 int32_t x, int32_t y, int32_t z) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
-        "l"(tmap), "r"(cluster_bar), "r"(x), "r"(y), "r"(z)
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(smem_dst),
+        "l"(tmap), "r"(cluster_bar), "r"(x), "r"(y), "r"(z), "r"((int)one)
         : "memory");
 }
 
@@ -173,62 +174,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ---------------- copy warp (both CTAs) ----------------
-        if (lane == 0) {
-            int it = 0;
-            for (int t = worker; t < total && !*abort_flag; t += workers) {
-                const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
-                const int half = ceil_div(w.n, 32) * 16;  // rows this CTA brings
-                const int wrow = w.e * a.N + w.ct * kCh + rank * 128;
-                const int xrow = w.row0 + rank * half;
-                const CUtensorMap* tx = &tmap_x.m[half / 16 - 1];
-                for (int kb = 0; kb < nkb; ++kb, ++it) {
-                    const int s = it % kStages;
-                    if (it >= kStages && !mbar_wait_cluster(&bar.empty[s], (uint32_t)(it / kStages - 1) & 1u, a.status)) {
-                        atomicExch(&bar.abort_flag, 1);
-                        break;
-                    }
-                    const int here = whole ? kAtoms : min(kAtoms, atoms - kb * kAtoms);
-                    if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], (uint32_t)(2 * here * (kATile + half * kKB)));
-                    const uint32_t full = map_rank(smem_u32(&bar.full[s]), 0);
-                    uint8_t* as = smem_a + s * kAtoms * kATile;
-                    uint8_t* bs = smem_b + s * kAtoms * kBTile;
-                    if (whole) {
-                        tma_load_3d_pair(as, &tmap_w, full, 0, wrow, kb * kAtoms);
-                        tma_load_3d_pair(bs, tx, full, 0, xrow, kb * kAtoms);
-                    } else {
-                        for (int at = 0; at < here; ++at) {
-                            const int x = (kb * kAtoms + at) * kKB;
-                            tma_load_3d_pair(as + at * kATile, &tmap_w, full, x, wrow, 0);
-                            tma_load_3d_pair(bs + at * half * kKB, tx, full, x, xrow, 0);
-                        }
+        const bool one = elect_one();
+        const uint32_t a0 = smem_u32(smem_a), b0 = smem_u32(smem_b);
+        const uint32_t full0 = map_rank(smem_u32(bar.full), 0);  // the leader's
+        int it = 0;
+        for (int t = worker; t < total && !__any_sync(0xffffffffu, *abort_flag); t += workers) {
+            const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
+            const int half = ceil_div(w.n, 32) * 16;  // rows this CTA brings
+            const int wrow = w.e * a.N + w.ct * kCh + rank * 128;
+            const int xrow = w.row0 + rank * half;
+            const CUtensorMap* tx = &tmap_x.m[half / 16 - 1];
+            for (int kb = 0; kb < nkb; ++kb, ++it) {
+                const int s = it % kStages;
+                if (it >= kStages &&
+                    !__all_sync(0xffffffffu, mbar_wait(&bar.empty[s], (uint32_t)(it / kStages - 1) & 1u, a.status))) {
+                    atomicExch(&bar.abort_flag, 1);
+                    break;
+                }
+                const int here = whole ? kAtoms : min(kAtoms, atoms - kb * kAtoms);
+                if (rank == 0 && one) mbar_arrive_expect_tx(&bar.full[s], (uint32_t)(2 * here * (kATile + half * kKB)));
+                const uint32_t full = full0 + 8 * s, as = a0 + s * kAtoms * kATile, bs = b0 + s * kAtoms * kBTile;
+                if (whole) {
+                    tma_load_3d_pair(one, as, &tmap_w, full, 0, wrow, kb * kAtoms);
+                    tma_load_3d_pair(one, bs, tx, full, 0, xrow, kb * kAtoms);
+                } else {
+                    for (int at = 0; at < here; ++at) {
+                        const int x = (kb * kAtoms + at) * kKB;
+                        tma_load_3d_pair(one, as + at * kATile, &tmap_w, full, x, wrow, 0);
+                        tma_load_3d_pair(one, bs + at * half * kKB, tx, full, x, xrow, 0);
                     }
                 }
             }
-            // before the pair ends, the loads in flight (of both CTAs) land in the
-            // leader's count and the leader's last arrivals reach the other CTA
-            for (int j = max(0, it - kStages); j < it; ++j) {
-                const uint32_t parity = (uint32_t)(j / kStages) & 1u;
-                if (rank == 0)
-                    mbar_wait(&bar.full[j % kStages], parity, a.status);
-                else
-                    mbar_wait_cluster(&bar.empty[j % kStages], parity, a.status);
-            }
+        }
+        // before the pair ends, the loads in flight (of both CTAs) land in the
+        // leader's count and the leader's last arrivals reach the other CTA
+        for (int j = max(0, it - kStages); j < it; ++j) {
+            const uint32_t parity = (uint32_t)(j / kStages) & 1u;
+            if (rank == 0)
+                mbar_wait(&bar.full[j % kStages], parity, a.status);
+            else
+                mbar_wait(&bar.empty[j % kStages], parity, a.status);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ---------------- MMA warp (leader) ----------------
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
+            const bool one = elect_one();
             int it = 0, ti = 0;
-            for (int t = worker; t < total && !*abort_flag; t += workers, ++ti) {
+            for (int t = worker; t < total && !__any_sync(0xffffffffu, *abort_flag); t += workers, ++ti) {
                 const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
                 const int half = ceil_div(w.n, 32) * 16;
                 const uint32_t idesc = mma_idesc_s8(kCh, 2 * half);
                 const int acc = ti & 1;
-                bool ok = ti < 2 || mbar_wait_cluster(&bar.acc_empty[acc], (uint32_t)((ti >> 1) - 1) & 1u, a.status);
+                bool ok = ti < 2 || __all_sync(0xffffffffu, mbar_wait_cluster(&bar.acc_empty[acc], (uint32_t)((ti >> 1) - 1) & 1u, a.status));
                 tc_fence_after();
                 for (int kb = 0; ok && kb < nkb; ++kb, ++it) {
                     const int s = it % kStages;
-                    ok = mbar_wait(&bar.full[s], (uint32_t)(it / kStages) & 1u, a.status);
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bar.full[s], (uint32_t)(it / kStages) & 1u, a.status));
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t ad = sw128_kmajor_desc(smem_u32(smem_a + s * kAtoms * kATile));
@@ -239,18 +241,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (at >= here) break;
 #pragma unroll
                         for (int kk = 0; kk < kKB / 32; ++kk)  // descriptors count 16-byte units
-                            tc_mma_i8_pair(tmem_base + (uint32_t)(acc * kMaxRows), ad + (at * kATile + kk * 32) / 16,
+                            tc_mma_i8_pair(one, tmem_base + (uint32_t)(acc * kMaxRows), ad + (at * kATile + kk * 32) / 16,
                                            bd + (at * half * kKB + kk * 32) / 16, idesc, (kb | at | kk) != 0 ? 1u : 0u);
                     }
-                    tc_commit_pair(&bar.empty[s], 3);
+                    if (one) tc_commit_pair(&bar.empty[s], 3);
                 }
                 if (!ok) {
                     atomicExch(&bar.abort_flag, 1);
                     break;
                 }
-                tc_commit_pair(&bar.acc_full[acc], 3);
+                if (one) tc_commit_pair(&bar.acc_full[acc], 3);
             }
-            tc_commit_pair(&bar.drain, 1);  // completes once every MMA issued above has
+            if (one) tc_commit_pair(&bar.drain, 1);  // completes once every MMA issued above has
             mbar_wait(&bar.drain, 0u, a.status);
         }
         __syncwarp();
@@ -262,7 +264,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int part = (warp - 2) >> 2;  // which half of the 64-column groups
         int ti = 0;
         for (int t = worker; t < total; t += workers, ++ti) {
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
             const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
             const int acc = ti & 1;
             float* rs = row_scale + acc * kMaxRows;
@@ -270,12 +271,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int c = w.ct * kCh + ch;
             const bool cv = c < a.N;
             const float sw = cv ? __half2float(__ushort_as_half(a.ws[(int64_t)w.e * a.N + c])) : 0.0f;
-            named_sync(1, 32 * kEpiWarps);
+            if (!named_sync_and(1, 32 * kEpiWarps, !*abort_flag)) break;
             const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bar.acc_full[acc], (uint32_t)(ti >> 1) & 1u, a.status));
             tc_fence_after();
             if (!ok) {
                 atomicExch(&bar.abort_flag, 1);
-                break;
+                continue;  // the next barrier ends the loop for all warps
             }
             const uint32_t dcol = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * kMaxRows);
             for (int c0 = 32 * part; c0 < w.n; c0 += 64) {
@@ -340,7 +341,8 @@ cudaError_t launch_w8a8_pair(const W8A8Args& a, int num_sms, bool pdl, cudaStrea
             cr = encode_tensor_map_k_atoms(&tx.m[half / 16 - 1], a.Xq, (uint64_t)a.K, (uint64_t)a.R, (uint32_t)half);
     if (cr != CUDA_SUCCESS) return cudaErrorInvalidValue;
     const int smem = pair_smem(a.E);
-    cudaError_t e = cudaFuncSetAttribute(w8a8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(w8a8_pair_kernel), 227 * 1024, allowed);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));

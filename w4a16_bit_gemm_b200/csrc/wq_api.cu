@@ -115,6 +115,17 @@ wq_status device_info(uint32_t** status, int* num_sms) {
     return WQ_OK;
 }
 
+cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (done.load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_release);
+    return e;
+}
+
 bool pdl_enabled() {
     static int v = -1;
     if (v < 0) {
