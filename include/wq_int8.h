@@ -14,9 +14,9 @@
  * dense row-major matrices, asynchronous calls on `stream`, argument errors
  * returned before anything is launched, conditions found on the device in the
  * status word, no device memory allocated, no other library called.  Every
- * entry point belongs to the current device; calls on several streams and
- * replays of captured graphs share nothing but the buffers that the caller
- * gives them (a workspace belongs to one call at a time).
+ * entry point belongs to the current device; none needs a workspace, so calls
+ * on several streams and replays of captured graphs share nothing but the
+ * buffers that the caller gives them.
  */
 #ifndef WQ_INT8_H_
 #define WQ_INT8_H_
@@ -124,36 +124,6 @@ wq_status wq_linear_w8a8(const int8_t* Xq, const float* x_scales, int64_t M, con
 wq_status wq_linear_w8a8_grouped(const int8_t* Xq, const float* x_scales, int64_t R, const int32_t* offsets, int64_t E,
                                  const uint32_t* qweight, const void* scales_fp16, int64_t d_out, int64_t d_in,
                                  void* Y, int32_t y_dtype, void* stream);
-
-/*
- * wq_linear_w8a8_bf16, wq_linear_w8a8_grouped_bf16 -- wq_quantize_tokens and
- * the product in one call, with the same result: for bf16 activations that
- * only this layer reads.  A few rows (decode) are quantized inside the
- * product's kernel, one launch in place of two; otherwise the codes and scales
- * go through the workspace.
- *
- *   X_bf16, T, rows, R, smooth_bf16: as wq_quantize_tokens (wq_linear_w8a8_bf16:
- *                 T = R = M, no rows).
- *   offsets, E, qweight, scales_fp16, d_out, d_in, Y, y_dtype: as the products.
- *   workspace     at least ..._workspace_bytes(...) bytes, 16-byte aligned (may
- *                 be NULL when that is 0).  Its contents on entry do not matter.
- * In the grouped form, rows of no expert need not be quantized: a bad index or
- * a non-finite value among them may go unreported.
- * Errors and device flags: those of both, and WQ_ERR_INVALID_ARG for a missing,
- * misaligned or small workspace.
- */
-wq_status wq_linear_w8a8_bf16(const void* X_bf16, int64_t M, const void* smooth_bf16, const uint32_t* qweight,
-                              const void* scales_fp16, int64_t d_out, int64_t d_in, void* Y, int32_t y_dtype,
-                              void* workspace, size_t workspace_bytes, void* stream);
-wq_status wq_linear_w8a8_grouped_bf16(const void* X_bf16, int64_t T, const int32_t* rows, int64_t R,
-                                      const void* smooth_bf16, const int32_t* offsets, int64_t E,
-                                      const uint32_t* qweight, const void* scales_fp16, int64_t d_out, int64_t d_in,
-                                      void* Y, int32_t y_dtype, void* workspace, size_t workspace_bytes,
-                                      void* stream);
-
-/* Scratch bytes of the two (0 when none is needed, and for invalid shapes). */
-size_t wq_linear_w8a8_bf16_workspace_bytes(int64_t M, int64_t d_out, int64_t d_in);
-size_t wq_linear_w8a8_grouped_bf16_workspace_bytes(int64_t R, int64_t E, int64_t d_out, int64_t d_in);
 
 #ifdef __cplusplus
 }

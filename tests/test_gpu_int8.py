@@ -257,7 +257,7 @@ def test_linear_whole_path_from_bf16():
 
 
 def check_linear_bf16(M, N, K, seed=0, dtype=torch.bfloat16, smooth=False, X=None):
-    """bf16 activations in one call, quantized inside the product or ahead of it."""
+    """bf16 activations in one call: quantized, then multiplied."""
     b = _b()
     X = activations(M, K, seed) if X is None else X
     sm = (torch.rand(K, generator=torch.Generator().manual_seed(seed)) + 0.2).to(torch.bfloat16) if smooth else None

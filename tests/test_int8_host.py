@@ -14,9 +14,7 @@ from tests import _int8_ref as ref
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 0x10000  # 16-byte aligned, never dereferenced: validation fails first
-ENTRY_POINTS = ["wq_linear_w8a8", "wq_linear_w8a8_bf16", "wq_linear_w8a8_grouped", "wq_linear_w8a8_grouped_bf16",
-                "wq_quantize_tokens"]
-SIZES = ["wq_linear_w8a8_bf16_workspace_bytes", "wq_linear_w8a8_grouped_bf16_workspace_bytes"]
+ENTRY_POINTS = ["wq_linear_w8a8", "wq_linear_w8a8_grouped", "wq_quantize_tokens"]
 
 
 @pytest.fixture(scope="module")
@@ -30,8 +28,8 @@ def b():
 def test_header_declares_what_the_library_exports(b):
     src = open(os.path.join(ROOT, "include", "wq_int8.h")).read()
     src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
-    assert sorted(set(re.findall(r"\b(wq_[a-z0-9_]+)\s*\(", src))) == sorted(ENTRY_POINTS + SIZES)
-    for n in ENTRY_POINTS + SIZES:
+    assert sorted(set(re.findall(r"\b(wq_[a-z0-9_]+)\s*\(", src))) == ENTRY_POINTS
+    for n in ENTRY_POINTS:
         assert hasattr(b.lib, n), n
     assert "WQ_DEVFLAG_INDEX 0x8u" in src and b.WQ_DEVFLAG_INDEX == 0x8
 
@@ -70,45 +68,6 @@ def test_linear_w8a8_grouped_rejects(b, case):
                                         a["Y"], a["ydt"], None) == 1
 
 
-BF16 = dict(X=FAKE, T=4, rows=None, R=4, smooth=None, q=FAKE, s=FAKE, N=64, K=256, Y=FAKE, ydt=0, ws=FAKE, wsb=1 << 20)
-BAD_BF16 = [dict(X=None), dict(X=FAKE + 8), dict(smooth=FAKE + 1), dict(q=None), dict(s=None), dict(N=0), dict(K=100),
-            dict(Y=None), dict(Y=FAKE + 4), dict(ydt=2)]
-
-
-@pytest.mark.parametrize("case", BAD_BF16 + [
-    dict(R=-1), dict(R=1 << 31),
-    # 4000 rows take a workspace
-    dict(R=4000, ws=None), dict(R=4000, wsb=4000 * 260 - 1), dict(R=4000, ws=FAKE + 8, wsb=1 << 30),
-])
-def test_linear_w8a8_bf16_rejects(b, case):
-    a = dict(BF16, **case)
-    assert b.lib.wq_linear_w8a8_bf16(a["X"], a["R"], a["smooth"], a["q"], a["s"], a["N"], a["K"], a["Y"], a["ydt"],
-                                     a["ws"], a["wsb"], None) == 1
-
-
-@pytest.mark.parametrize("case", BAD_BF16 + [
-    dict(rows=FAKE + 2), dict(T=5), dict(rows=FAKE, R=-1), dict(off=None), dict(E=0), dict(E=1000, N=1 << 22),
-    dict(T=4000, R=4000, ws=None), dict(T=4000, R=4000, wsb=100),
-])
-def test_linear_w8a8_grouped_bf16_rejects(b, case):
-    a = dict(BF16, off=FAKE, E=8)
-    a.update(case)
-    assert b.lib.wq_linear_w8a8_grouped_bf16(a["X"], a["T"], a["rows"], a["R"], a["smooth"], a["off"], a["E"], a["q"],
-                                             a["s"], a["N"], a["K"], a["Y"], a["ydt"], a["ws"], a["wsb"], None) == 1
-
-
-def test_workspace_sizes(b):
-    dense, grouped = b.wq_linear_w8a8_bf16_workspace_bytes, b.wq_linear_w8a8_grouped_bf16_workspace_bytes
-    assert dense(4000, 64, 256) == 4000 * 260 and grouped(4000, 8, 64, 256) == 4000 * 260
-    assert dense(1, 4096, 4096) == 0 and dense(16, 11008, 4096) == 0  # quantized inside the product
-    for M in (1, 5, 16, 17, 300):
-        for N, K in ((64, 32), (4096, 11008), (28672, 8192), (1000, 131040)):
-            assert dense(M, N, K) in (0, M * (K + 4))
-            for E in (1, 8, 1024):
-                assert grouped(M, E, N, K) in (0, M * (K + 4))
-    assert dense(0, 64, 256) == dense(4, 64, 100) == grouped(4, 0, 64, 256) == grouped(4, 2000, 64, 256) == 0
-
-
 def test_too_many_experts_is_unsupported(b):
     assert b.lib.wq_linear_w8a8_grouped(FAKE, FAKE, 4, FAKE, 1025, FAKE, FAKE, 64, 256, FAKE, 0, None) == 2
 
@@ -125,8 +84,6 @@ def call(name, *args):
 call("wq_quantize_tokens", F, 4, 256, None, 4, None, F, F, None)
 call("wq_linear_w8a8", F, F, 4, F, F, 64, 256, F, 0, None)
 call("wq_linear_w8a8_grouped", F, F, 4, F, 8, F, F, 64, 256, F, 0, None)
-call("wq_linear_w8a8_bf16", F, 4, None, F, F, 64, 256, F, 0, F, 1 << 20, None)
-call("wq_linear_w8a8_grouped_bf16", F, 4, None, 4, None, F, 8, F, F, 64, 256, F, 0, F, 1 << 20, None)
 before = lib.wq_fault_injections()
 out["invalid"] = [lib.wq_linear_w8a8(None, F, 4, F, F, 64, 256, F, 0, None), lib.wq_fault_injections() - before]
 print(json.dumps(out))

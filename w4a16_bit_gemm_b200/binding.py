@@ -85,14 +85,6 @@ def _load() -> ctypes.CDLL:
     lib.wq_linear_w8a8.restype = ctypes.c_int
     lib.wq_linear_w8a8_grouped.argtypes = [P, P, i64, P, i64, P, P, i64, i64, P, i32, P]
     lib.wq_linear_w8a8_grouped.restype = ctypes.c_int
-    lib.wq_linear_w8a8_bf16.argtypes = [P, i64, P, P, P, i64, i64, P, i32, P, sz, P]
-    lib.wq_linear_w8a8_bf16.restype = ctypes.c_int
-    lib.wq_linear_w8a8_grouped_bf16.argtypes = [P, i64, P, i64, P, P, i64, P, P, i64, i64, P, i32, P, sz, P]
-    lib.wq_linear_w8a8_grouped_bf16.restype = ctypes.c_int
-    lib.wq_linear_w8a8_bf16_workspace_bytes.argtypes = [i64, i64, i64]
-    lib.wq_linear_w8a8_bf16_workspace_bytes.restype = sz
-    lib.wq_linear_w8a8_grouped_bf16_workspace_bytes.argtypes = [i64, i64, i64, i64]
-    lib.wq_linear_w8a8_grouped_bf16_workspace_bytes.restype = sz
     lib.wq_get_device_error.argtypes = [P, P]
     lib.wq_get_device_error.restype = ctypes.c_int
     lib.wq_selftest_bounded_wait.argtypes = [ctypes.c_uint32, P]
@@ -204,27 +196,6 @@ def wq_linear_w8a8(Xq, x_scales, M, qweight, scales, d_out, d_in, Y, y_dtype, st
 def wq_linear_w8a8_grouped(Xq, x_scales, R, offsets, E, qweight, scales, d_out, d_in, Y, y_dtype, stream=None) -> int:
     return lib.wq_linear_w8a8_grouped(_ptr(Xq), _ptr(x_scales), R, _ptr(offsets), E, _ptr(qweight), _ptr(scales),
                                       d_out, d_in, _ptr(Y), y_dtype, _stream(stream))
-
-
-def wq_linear_w8a8_bf16(X, M, smooth, qweight, scales, d_out, d_in, Y, y_dtype, workspace=None, workspace_bytes=0,
-                        stream=None) -> int:
-    return lib.wq_linear_w8a8_bf16(_ptr(X), M, _ptr(smooth), _ptr(qweight), _ptr(scales), d_out, d_in, _ptr(Y), y_dtype,
-                                   _ptr(workspace), workspace_bytes, _stream(stream))
-
-
-def wq_linear_w8a8_grouped_bf16(X, T, rows, R, smooth, offsets, E, qweight, scales, d_out, d_in, Y, y_dtype,
-                                workspace=None, workspace_bytes=0, stream=None) -> int:
-    return lib.wq_linear_w8a8_grouped_bf16(_ptr(X), T, _ptr(rows), R, _ptr(smooth), _ptr(offsets), E, _ptr(qweight),
-                                           _ptr(scales), d_out, d_in, _ptr(Y), y_dtype, _ptr(workspace),
-                                           workspace_bytes, _stream(stream))
-
-
-def wq_linear_w8a8_bf16_workspace_bytes(M, d_out, d_in) -> int:
-    return int(lib.wq_linear_w8a8_bf16_workspace_bytes(M, d_out, d_in))
-
-
-def wq_linear_w8a8_grouped_bf16_workspace_bytes(R, E, d_out, d_in) -> int:
-    return int(lib.wq_linear_w8a8_grouped_bf16_workspace_bytes(R, E, d_out, d_in))
 
 
 def wq_gptq(W, d_out, d_in, X, T, group_size, symmetric, act_order, qweight, scales, zeros, perm, workspace,
@@ -472,26 +443,38 @@ def quantize_tokens(X: torch.Tensor, rows: torch.Tensor | None = None, smooth: t
     return out
 
 
-def _codes_operands(x, d_in, rows, smooth, device):
-    """Checked row count of activations that are quantized already."""
-    if rows is not None or smooth is not None:
-        raise ValueError("rows and smooth apply to bf16 activations; these are quantized already")
-    R = x.codes.shape[0]
-    _expect("x.codes", x.codes, torch.int8, (R, d_in), device)
-    _expect("x.scales", x.scales, torch.float32, (R,), device)
-    return R
+def _w8a8_activations(x, rows, smooth, d_in, device):
+    """(codes pointer, scales pointer, rows, buffer) of a product's INT8
+    activations: given, or quantized from bf16 into a buffer that the caller
+    keeps until the product is queued.  Runs on the current device and stream."""
+    if isinstance(x, QuantizedTokens):
+        if rows is not None or smooth is not None:
+            raise ValueError("rows and smooth apply to bf16 activations; these are quantized already")
+        R = x.codes.shape[0]
+        _expect("x.codes", x.codes, torch.int8, (R, d_in), device)
+        _expect("x.scales", x.scales, torch.float32, (R,), device)
+        return x.codes.data_ptr(), x.scales.data_ptr(), R, None
+    T, k, R = _token_operands(x, rows, smooth)
+    if k != d_in or x.device != device:
+        raise ValueError(f"x must be a contiguous [tokens, {d_in}] bf16 tensor on {device}")
+    buf = x.new_empty(R * (d_in + 4) // 2)  # codes, then scales (d_in is a multiple of 32), in 2-byte elements
+    codes = buf.data_ptr()
+    scales = codes + R * d_in
+    _check(lib.wq_quantize_tokens(x.data_ptr(), T, d_in, _ptr(rows), R, _ptr(smooth), codes, scales,
+                                  _current_raw_stream(device.index)), "wq_quantize_tokens")
+    return codes, scales, R, buf
 
 
-def _w8a8_output(out, out_dtype, shape, device):
+def _w8a8_output(out, out_dtype, shape, like):
     if out is None:
         out_dtype = out_dtype or torch.bfloat16
         if out_dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
-        out = torch.empty(shape, dtype=out_dtype, device=device)
+        out = like.new_empty(shape, dtype=out_dtype)
     else:
         if out.dtype not in (torch.bfloat16, torch.float32) or (out_dtype or out.dtype) != out.dtype:
             raise ValueError("out must be a bf16 or fp32 tensor (of out_dtype, when both are given)")
-        _expect("out", out, out.dtype, shape, device)
+        _expect("out", out, out.dtype, shape, like.device)
     return out, (WQ_OUT_FP32 if out.dtype is torch.float32 else WQ_OUT_BF16)
 
 
@@ -514,22 +497,10 @@ def linear_w8a8(x, p: PackedLinearW8, out_dtype=None, out: torch.Tensor | None =
     if there is not None:
         with there:
             return linear_w8a8(x, p, out_dtype, out, smooth)
-    if isinstance(x, QuantizedTokens):
-        M = _codes_operands(x, d_in, None, smooth, device)
-        out, y_dtype = _w8a8_output(out, out_dtype, (M, d_out), device)
-        _check(lib.wq_linear_w8a8(x.codes.data_ptr(), x.scales.data_ptr(), M, qweight.data_ptr(), scales.data_ptr(),
-                                  d_out, d_in, out.data_ptr(), y_dtype, _current_raw_stream(device.index)),
-               "wq_linear_w8a8")
-        return out
-    M, k, _ = _token_operands(x, None, smooth)
-    if k != d_in or x.device != device:
-        raise ValueError(f"x must be a contiguous [tokens, {d_in}] bf16 tensor on {device}")
-    out, y_dtype = _w8a8_output(out, out_dtype, (M, d_out), device)
-    need = lib.wq_linear_w8a8_bf16_workspace_bytes(M, d_out, d_in)
-    workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    _check(lib.wq_linear_w8a8_bf16(x.data_ptr(), M, _ptr(smooth), qweight.data_ptr(), scales.data_ptr(), d_out, d_in,
-                                   out.data_ptr(), y_dtype, _ptr(workspace), need,
-                                   _current_raw_stream(device.index)), "wq_linear_w8a8_bf16")
+    codes, x_scales, M, _buf = _w8a8_activations(x, None, smooth, d_in, device)
+    out, y_dtype = _w8a8_output(out, out_dtype, (M, d_out), scales)
+    _check(lib.wq_linear_w8a8(codes, x_scales, M, qweight.data_ptr(), scales.data_ptr(), d_out, d_in, out.data_ptr(),
+                              y_dtype, _current_raw_stream(device.index)), "wq_linear_w8a8")
     return out
 
 
@@ -553,23 +524,11 @@ def linear_w8a8_grouped(x, p: PackedExpertsW8, offsets: torch.Tensor, out_dtype=
     if there is not None:
         with there:
             return linear_w8a8_grouped(x, p, offsets, out_dtype, out, rows, smooth)
-    if isinstance(x, QuantizedTokens):
-        R = _codes_operands(x, d_in, rows, smooth, device)
-        out, y_dtype = _w8a8_output(out, out_dtype, (R, d_out), device)
-        _check(lib.wq_linear_w8a8_grouped(x.codes.data_ptr(), x.scales.data_ptr(), R, offsets.data_ptr(), E,
-                                          qweight.data_ptr(), scales.data_ptr(), d_out, d_in, out.data_ptr(), y_dtype,
-                                          _current_raw_stream(device.index)), "wq_linear_w8a8_grouped")
-        return out
-    T, k, R = _token_operands(x, rows, smooth)
-    if k != d_in or x.device != device:
-        raise ValueError(f"x must be a contiguous [tokens, {d_in}] bf16 tensor on {device}")
-    out, y_dtype = _w8a8_output(out, out_dtype, (R, d_out), device)
-    need = lib.wq_linear_w8a8_grouped_bf16_workspace_bytes(R, E, d_out, d_in)
-    workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    _check(lib.wq_linear_w8a8_grouped_bf16(x.data_ptr(), T, _ptr(rows), R, _ptr(smooth), offsets.data_ptr(), E,
-                                           qweight.data_ptr(), scales.data_ptr(), d_out, d_in, out.data_ptr(), y_dtype,
-                                           _ptr(workspace), need, _current_raw_stream(device.index)),
-           "wq_linear_w8a8_grouped_bf16")
+    codes, x_scales, R, _buf = _w8a8_activations(x, rows, smooth, d_in, device)
+    out, y_dtype = _w8a8_output(out, out_dtype, (R, d_out), scales)
+    _check(lib.wq_linear_w8a8_grouped(codes, x_scales, R, offsets.data_ptr(), E, qweight.data_ptr(),
+                                      scales.data_ptr(), d_out, d_in, out.data_ptr(), y_dtype,
+                                      _current_raw_stream(device.index)), "wq_linear_w8a8_grouped")
     return out
 
 

@@ -67,7 +67,8 @@ wq_status status_of(cudaError_t e) {
 // SMs.  Measured on both sides: see the kernels.
 cudaError_t run_product(const W8A8Args& a, int num_sms, cudaStream_t stream) {
     const int mean = a.R / (a.E < a.R ? a.E : a.R);
-    return mean <= 64 ? launch_w8a8_stream(a, pdl_enabled(), stream) : launch_w8a8_pair(a, num_sms, pdl_enabled(), stream);
+    const auto launch = mean <= 64 ? launch_w8a8_stream : launch_w8a8_pair;
+    return launch(a, num_sms, pdl_enabled(), stream);
 }
 
 wq_status product_of_codes(W8A8Args a, const int8_t* Xq, const float* x_scales, void* stream) {
@@ -78,38 +79,6 @@ wq_status product_of_codes(W8A8Args a, const int8_t* Xq, const float* x_scales, 
     a.Xq = Xq;
     a.xs = x_scales;
     return status_of(run_product(a, num_sms, static_cast<cudaStream_t>(stream)));
-}
-
-// bf16 rows: quantized inside the product where that fits, else into the
-// workspace (codes, then scales).
-wq_status product_of_bf16(W8A8Args a, const void* X, int64_t T, const int32_t* rows, const void* smooth, void* workspace,
-                          size_t workspace_bytes, size_t needed, void* stream) {
-    if (workspace_bytes < needed || (needed > 0 && (!workspace || !aligned(workspace, 16)))) return WQ_ERR_INVALID_ARG;
-    int num_sms = 0;
-    const wq_status v = device_info(&a.status, &num_sms);
-    if (v != WQ_OK) return v;
-    if (a.R == 0) return WQ_OK;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (needed == 0) {
-        a.X = static_cast<const uint16_t*>(X);
-        a.rows = rows;
-        a.smooth = static_cast<const uint16_t*>(smooth);
-        a.T = (int)T;
-        return status_of(launch_w8a8_rows(a, pdl_enabled(), s));
-    }
-    int8_t* codes = static_cast<int8_t*>(workspace);
-    float* scales = reinterpret_cast<float*>(codes + (int64_t)a.R * a.K);
-    const cudaError_t e = launch_quantize_tokens(X, T, a.K, rows, a.R, smooth, codes, scales, a.status, pdl_enabled(), s);
-    if (e != cudaSuccess) return WQ_ERR_CUDA;
-    a.Xq = codes;
-    a.xs = scales;
-    return status_of(run_product(a, num_sms, s));
-}
-
-size_t bf16_workspace(int64_t R, int64_t E, bool grouped, int64_t d_out, int64_t d_in) {
-    if (R < 1 || R > kMaxInt32 || E < 1 || E > WQ_INT8_MAX_EXPERTS || d_out < 1 || d_out > kMaxInt32 || !depth_ok(d_in))
-        return 0;
-    return w8a8_rows_fit(R, E, grouped, d_out, d_in) ? 0 : (size_t)(R * (d_in + 4));
 }
 
 }  // namespace
@@ -150,39 +119,6 @@ wq_status wq_linear_w8a8_grouped(const int8_t* Xq, const float* x_scales, int64_
     if (v != WQ_OK) return v;
     return product_of_codes(product_args(R, offsets, E, qweight, scales_fp16, d_out, d_in, Y, y_dtype), Xq, x_scales,
                             stream);
-}
-
-size_t wq_linear_w8a8_bf16_workspace_bytes(int64_t M, int64_t d_out, int64_t d_in) {
-    return bf16_workspace(M, 1, false, d_out, d_in);
-}
-
-size_t wq_linear_w8a8_grouped_bf16_workspace_bytes(int64_t R, int64_t E, int64_t d_out, int64_t d_in) {
-    return bf16_workspace(R, E, true, d_out, d_in);
-}
-
-wq_status wq_linear_w8a8_bf16(const void* X_bf16, int64_t M, const void* smooth_bf16, const uint32_t* qweight,
-                              const void* scales_fp16, int64_t d_out, int64_t d_in, void* Y, int32_t y_dtype,
-                              void* workspace, size_t workspace_bytes, void* stream) {
-    wq_status v = check_product(M, qweight, scales_fp16, d_out, d_in, Y, y_dtype);
-    if (v == WQ_OK) v = check_tokens(X_bf16, M, d_in, nullptr, M, smooth_bf16);
-    if (v != WQ_OK) return v;
-    return product_of_bf16(product_args(M, nullptr, 1, qweight, scales_fp16, d_out, d_in, Y, y_dtype), X_bf16, M,
-                           nullptr, smooth_bf16, workspace, workspace_bytes,
-                           wq_linear_w8a8_bf16_workspace_bytes(M, d_out, d_in), stream);
-}
-
-wq_status wq_linear_w8a8_grouped_bf16(const void* X_bf16, int64_t T, const int32_t* rows, int64_t R,
-                                      const void* smooth_bf16, const int32_t* offsets, int64_t E,
-                                      const uint32_t* qweight, const void* scales_fp16, int64_t d_out, int64_t d_in,
-                                      void* Y, int32_t y_dtype, void* workspace, size_t workspace_bytes,
-                                      void* stream) {
-    wq_status v = check_product(R, qweight, scales_fp16, d_out, d_in, Y, y_dtype);
-    if (v == WQ_OK) v = check_tokens(X_bf16, T, d_in, rows, R, smooth_bf16);
-    if (v == WQ_OK) v = check_experts(offsets, E, d_out);
-    if (v != WQ_OK) return v;
-    return product_of_bf16(product_args(R, offsets, E, qweight, scales_fp16, d_out, d_in, Y, y_dtype), X_bf16, T, rows,
-                           smooth_bf16, workspace, workspace_bytes,
-                           wq_linear_w8a8_grouped_bf16_workspace_bytes(R, E, d_out, d_in), stream);
 }
 
 }  // extern "C"

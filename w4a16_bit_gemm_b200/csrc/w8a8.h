@@ -39,11 +39,6 @@ struct W8A8Args {
     uint32_t* status;
     int R, N, K, E;
     int y_fp32;
-    // for launch_w8a8_rows, in place of Xq and xs: activations to quantize
-    const uint16_t* X;        // bf16 [T][K]
-    const int32_t* rows;      // [R] or nullptr (row r is X row r)
-    const uint16_t* smooth;   // bf16 [K] or nullptr
-    int T;
 };
 
 // Sets a kernel's shared-memory limit once per device (the call costs 1.4 us).
@@ -51,13 +46,7 @@ cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<uint6
 
 // Few rows per weight matrix: one CTA per tile of 128 channels, K split over a
 // cluster when there are few tiles (w8a8_stream.cu).
-cudaError_t launch_w8a8_stream(const W8A8Args& a, bool pdl, cudaStream_t stream);
-
-// The same for bf16 rows that the kernel quantizes itself, one launch in place
-// of two; for products small enough that every CTA has one tile and its rows'
-// codes fit beside the weights (w8a8_rows_fit; the same answer on every device).
-bool w8a8_rows_fit(int64_t R, int64_t E, bool grouped, int64_t N, int64_t K);
-cudaError_t launch_w8a8_rows(const W8A8Args& a, bool pdl, cudaStream_t stream);
+cudaError_t launch_w8a8_stream(const W8A8Args& a, int num_sms, bool pdl, cudaStream_t stream);
 
 // Many rows per weight matrix: pairs of CTAs share tiles of 256 channels x up
 // to 256 rows (w8a8_pair.cu).

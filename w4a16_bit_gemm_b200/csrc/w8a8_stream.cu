@@ -17,13 +17,6 @@
 // and adds up its own.  Integer sums do not depend on their order, so the
 // result is the same for every split.
 //
-// The same kernel takes bf16 rows (kQuantize): while the weights are on their
-// way, the epilogue warps find the rows' maxima over this CTA's part of K,
-// the cluster exchanges them, and the codes are written straight into the
-// layout that the MMA reads (every CTA does this for its own part of K; a few
-// rows are cheap next to 128 channels of weights).  One launch in place of two
-// for a decode step that holds bf16 activations.
-//
 // For one weight matrix, the first weights are requested before the wait for
 // the previous kernel (programmatic dependent launch): they do not depend on
 // it, the activations do.  What follows the wait is kept short: one load of
@@ -31,7 +24,6 @@
 // (WQ_DEVFLAG_TIMEOUT).
 #include <stdint.h>
 
-#include "tokens_device.cuh"
 #include "w8a8.h"
 #include "w8a8_device.cuh"
 #include "wq_kernels.h"
@@ -55,22 +47,11 @@ struct StreamPlan {
     int n_ct;     // channel tiles
     int grid;
     int smem;
-    int b_rows;   // kQuantize: rows of the code tile, 8 or 16
-    int b_atoms;  // kQuantize: atoms of the code tile (this CTA's part of K)
 };
 
 // Boxes of 16, 32, 48 and 64 rows: a tile's rows rounded up to 16, in one copy.
 struct RowMaps {
     CUtensorMap m[kMaxRows / 16];
-};
-
-constexpr int kOwnRows = 16;  // kQuantize: most rows of a tile
-
-struct OwnRows {
-    int src[kOwnRows];                       // row of X, -1 for a bad index
-    uint32_t amax[kOwnRows];                 // largest finite |x| of this part of K, bf16 bits
-    uint32_t amax_of[kMaxSplit][kOwnRows];   // ... of the cluster's CTAs
-    float rcp[kOwnRows];
 };
 
 struct StreamBars {
@@ -80,11 +61,8 @@ struct StreamBars {
     uint64_t acc_empty[2];
     uint64_t recv;
     uint64_t drain;
-    uint64_t codes;    // kQuantize: the code tile is written
-    uint64_t maxima;   // kQuantize: the others' maxima have arrived
     uint32_t tmem_slot;
     int abort_flag;
-    OwnRows own;
 };
 
 __host__ __device__ constexpr int table_ints(int E) { return (E + 1 + 3) & ~3; }
@@ -97,131 +75,6 @@ __host__ __device__ constexpr int tail_bytes(int nt, int split, int E) {
     return recv_bytes(nt, split) + 2 * nt * 4 + 2 * table_ints(E) * 4 + 64 * 4 + (int)sizeof(StreamBars);
 }
 
-// Codes of the tile's rows row0 .. row0 + n - 1 over columns [k_lo, k_hi) into
-// the code tile (atoms of b_rows x 128 bytes, SWIZZLE_128B), their scales into
-// rs.  Called by the four epilogue warps, which all pass its barriers even
-// where a wait gives up (false then).
-__device__ __forceinline__ bool quantize_own_rows(const W8A8Args& a, const StreamPlan& p, StreamBars& bar, int row0, int n,
-                                                  int k_lo, int k_hi, int rank, uint8_t* code_tile, float* rs) {
-    const int ew = (int)(threadIdx.x >> 5) - 2, lane = threadIdx.x & 31, et = (int)threadIdx.x - 64;
-    OwnRows& o = bar.own;
-    if (et < n) {
-        int src = row0 + et;
-        if (a.rows) {
-            src = a.rows[src];
-            if (src < 0 || src >= a.T) {
-                src = -1;
-                raise_flag(a.status, WQ_DEVFLAG_INDEX);
-            }
-        }
-        o.src[et] = src;
-    }
-    if (et < kOwnRows) o.amax[et] = 0u;
-    if (et == 0 && p.split > 1) mbar_arrive_expect_tx(&bar.maxima, (uint32_t)((p.split - 1) * kOwnRows * 4));
-    named_sync(1, 128);
-    // warps per row, and this warp's rows and columns
-    const int team = n == 1 ? 4 : n == 2 ? 2 : 1;
-    const int first = ew / team, step = 4 / team;
-    const int pieces = (k_hi - k_lo) / 8;
-    const int l0 = (ew % team) * 32 + lane, stride = team * 32;
-    const int per_row = (pieces + stride - 1) / stride;
-    const int items = (n - first + step - 1) / step * per_row;  // <= 0: no row for this warp
-    constexpr int kBatch = 8;
-    uint4 v[kBatch];
-    bool finite = true;
-    const auto load = [&](int item0) {
-        int i = first + item0 / per_row * step, l = l0 + item0 % per_row * stride;
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            v[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (item0 + u < items && l < pieces && o.src[i] >= 0)
-                v[u] = load_row16(a.X + (int64_t)o.src[i] * a.K + k_lo + 8 * l);
-            l += stride;
-            if (l >= l0 + per_row * stride) {
-                l = l0;
-                i += step;
-            }
-        }
-        if (a.smooth) {
-            i = first + item0 / per_row * step, l = l0 + item0 % per_row * stride;
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                if (item0 + u < items && l < pieces && o.src[i] >= 0)
-                    v[u] = smooth8_exact(v[u], load_smooth(a.smooth, k_lo + 8 * l));
-                l += stride;
-                if (l >= l0 + per_row * stride) {
-                    l = l0;
-                    i += step;
-                }
-            }
-        }
-    };
-    for (int item0 = 0; item0 < items; item0 += kBatch) {
-        load(item0);
-        int i = first + item0 / per_row * step, l = item0 % per_row;
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            if (item0 + u < items) {
-                float m = 0.0f, bad = 0.0f;
-                finite_max8(v[u], m, bad);
-                if (bad != 0.0f) finite = false;
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m) >> 16);
-                if (lane == 0) atomicMax(&o.amax[i], top);
-                if (++l == per_row) {
-                    l = 0;
-                    i += step;
-                }
-            }
-        }
-    }
-    if (!finite) raise_flag(a.status, WQ_DEVFLAG_NONFINITE);
-    named_sync(1, 128);
-    bool ok = true;
-    if (p.split > 1) {
-        if (et < kOwnRows) {
-            const uint32_t at = smem_u32(&o.amax_of[rank][et]), landed = smem_u32(&bar.maxima);
-            for (int r = 0; r < p.split; ++r)
-                if (r != rank) st_async_b32(map_rank(at, (uint32_t)r), o.amax[et], map_rank(landed, (uint32_t)r));
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(&bar.maxima, 0u, a.status));
-    }
-    if (et < n) {
-        uint32_t m = o.amax[et];
-        for (int r = 0; r < p.split; ++r)
-            if (r != rank) m = max(m, o.amax_of[r][et]);
-        const float s = token_scale(__uint_as_float(m << 16));
-        rs[et] = s;
-        o.rcp[et] = __frcp_rn(s);
-    }
-    named_sync(1, 128);
-    for (int item0 = 0; item0 < items; item0 += kBatch) {
-        if (items > kBatch) load(item0);
-        int i = first + item0 / per_row * step, l = l0 + item0 % per_row * stride;
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            if (item0 + u < items) {
-                if (l < pieces) {
-                    const float s = rs[i];
-                    const uint2 q = codes8(v[u], s, o.rcp[i], finite && s >= kFastScale);
-                    // 8 codes: half h of the 16-byte chunk c of row i in its atom
-                    const int atom = l >> 4, c = (l >> 1) & 7, h = l & 1;
-                    *reinterpret_cast<uint2*>(code_tile + atom * p.b_rows * kAtom + i * kAtom + ((c ^ (i & 7)) << 4) + 8 * h) = q;
-                }
-                l += stride;
-                if (l >= l0 + per_row * stride) {
-                    l = l0;
-                    i += step;
-                }
-            }
-        }
-    }
-    fence_proxy_async_smem();  // the MMA reads the codes through the async proxy
-    __syncwarp();
-    if (lane == 0 && ok) mbar_arrive(&bar.codes);
-    return ok;
-}
-
-template <bool kQuantize>
 __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_constant__ RowMaps tmap_x,
                                                                const __grid_constant__ CUtensorMap tmap_w,
                                                                const W8A8Args a, const StreamPlan p) {
@@ -230,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
     const int b_tile = p.nt * kAtom;
     uint8_t* smem_a = smem;
     uint8_t* smem_b = smem + p.stages * kAtoms * kATile;
-    uint8_t* tail = smem_b + (kQuantize ? p.b_atoms * p.b_rows * kAtom : p.stages * kAtoms * b_tile);
+    uint8_t* tail = smem_b + p.stages * kAtoms * b_tile;
     uint4* recv = reinterpret_cast<uint4*>(tail);  // [sender][own group][channel]
     float* row_scale = reinterpret_cast<float*>(tail + recv_bytes(p.nt, p.split));  // [2][nt]
     int* off = reinterpret_cast<int*>(row_scale + 2 * p.nt);
@@ -258,8 +111,6 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
         }
         mbar_init(&bar.recv, 1);
         mbar_init(&bar.drain, 1);
-        mbar_init(&bar.codes, 4);
-        mbar_init(&bar.maxima, 1);
         bar.abort_flag = 0;
         fence_mbar_init();
     }
@@ -290,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
             const int wrow = w.e * a.N + w.ct * kCh;
             const auto expect = [&](int s, int kb) {
                 const int here = whole ? kAtoms : min(kAtoms, atoms - kb * kAtoms);
-                if (one) mbar_arrive_expect_tx(&bar.full[s], (uint32_t)(here * (kATile + (kQuantize ? 0 : rows * kAtom))));
+                if (one) mbar_arrive_expect_tx(&bar.full[s], (uint32_t)(here * (kATile + rows * kAtom)));
             };
             const auto load = [&](uint32_t dst, int atom_bytes, const CUtensorMap* map, int s, int kb, int row) {
                 if (whole) {
@@ -307,10 +158,8 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
                     expect(i, kb0 + i);
                     load(a0 + i * kAtoms * kATile, kATile, &tmap_w, i, kb0 + i, wrow);
                 }
-                if constexpr (!kQuantize) {
-                    prefetch_tmap(tx);
-                    pdl_wait_prior();
-                }
+                prefetch_tmap(tx);
+                pdl_wait_prior();
                 waited = true;
             }
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
@@ -324,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
                     expect(s, kb);
                     load(a0 + s * kAtoms * kATile, kATile, &tmap_w, s, kb, wrow);
                 }
-                if constexpr (!kQuantize) load(b0 + s * kAtoms * b_tile, rows * kAtom, tx, s, kb, w.row0);
+                load(b0 + s * kAtoms * b_tile, rows * kAtom, tx, s, kb, w.row0);
             }
         }
         // the loads in flight land before the CTA ends
@@ -338,17 +187,15 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
             int it = 0, ti = 0;
             for (int t = worker; t < total && !__any_sync(0xffffffffu, *abort_flag); t += workers, ++ti) {
                 const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 16);
-                const int rows = kQuantize ? p.b_rows : (w.n + 15) & ~15;
+                const int rows = (w.n + 15) & ~15;
                 const uint32_t idesc = mma_idesc_s8(kCh, rows);
                 const int acc = ti & 1;
                 bool ok = ti < 2 || __all_sync(0xffffffffu, mbar_wait(&bar.acc_empty[acc], (uint32_t)((ti >> 1) - 1) & 1u, a.status));
-                if constexpr (kQuantize) ok = ok && __all_sync(0xffffffffu, mbar_wait(&bar.codes, 0u, a.status));
                 tc_fence_after();
                 for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
                     const int s = it % p.stages;
                     const uint64_t ad = sw128_kmajor_desc(smem_u32(smem_a + s * kAtoms * kATile));
-                    const uint64_t bd = sw128_kmajor_desc(
-                        smem_u32(smem_b + (kQuantize ? (kb - kb0) * kAtoms * rows * kAtom : s * kAtoms * b_tile)));
+                    const uint64_t bd = sw128_kmajor_desc(smem_u32(smem_b + s * kAtoms * b_tile));
                     const int here = min(kAtoms, atoms - kb * kAtoms);
                     ok = __all_sync(0xffffffffu, mbar_wait(&bar.full[s], (uint32_t)(it / p.stages) & 1u, a.status));
                     if (!ok) break;
@@ -401,18 +248,9 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
                 waited = true;
             }
             float* rs = row_scale + acc * p.nt;
-            bool ok = true;
-            if constexpr (kQuantize) {
-                ok = quantize_own_rows(a, p, bar, w.row0, w.n, kb0 * kAtoms * kAtom, min(kb1 * kAtoms * kAtom, a.K), rank,
-                                       smem_b, rs);
-            } else if (et < w.n) {
-                rs[et] = a.xs[w.row0 + et];
-            }
-            if (!named_sync_and(1, 128, ok && !*abort_flag)) {
-                atomicExch(&bar.abort_flag, 1);
-                break;
-            }
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar.acc_full[acc], (uint32_t)(ti >> 1) & 1u, a.status));
+            if (et < w.n) rs[et] = a.xs[w.row0 + et];
+            if (!named_sync_and(1, 128, !*abort_flag)) break;
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(&bar.acc_full[acc], (uint32_t)(ti >> 1) & 1u, a.status));
             tc_fence_after();
             if (!ok) {
                 atomicExch(&bar.abort_flag, 1);
@@ -497,61 +335,43 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
     }
 }
 
-}  // namespace
-
-namespace {
-
-constexpr int kSms = 148;            // the plan does not ask the device: a workspace size follows from it
 constexpr int kCtaSmem = 112 * 1024;  // two CTAs per SM
 
-// Tiles, split and shared memory of a product; false if it does not fit.
-bool plan_stream(StreamPlan& p, int64_t R, int64_t E, bool grouped, int64_t N, int64_t K, bool quantize) {
-    const int64_t experts = E < R ? E : R;  // that can have rows
-    const int64_t per_expert = (R + experts - 1) / experts;
-    p.n_ct = (int)((N + kCh - 1) / kCh);
+}  // namespace
+
+cudaError_t launch_w8a8_stream(const W8A8Args& a, int num_sms, bool pdl, cudaStream_t stream) {
+    StreamPlan p = {};
+    p.n_ct = ceil_div(a.N, kCh);
+    const int experts = a.E < a.R ? a.E : a.R;  // that can have rows
+    const int per_expert = ceil_div(a.R, experts);
     // rows per tile: what an expert holds, with room for an uneven share
     p.nt = 16;
-    while (!quantize && p.nt < kMaxRows && p.nt < (grouped ? 2 * per_expert : per_expert)) p.nt *= 2;
-    const int64_t tiles = (grouped ? experts + R / p.nt : (R + p.nt - 1) / p.nt) * p.n_ct;
-    if (tiles > 0x7fffffff) return false;
-    const int nkb = (int)((K + kAtom * kAtoms - 1) / (kAtom * kAtoms));
-    constexpr int64_t slots = 2 * kSms;
+    while (p.nt < kMaxRows && p.nt < (a.offsets ? 2 * per_expert : per_expert)) p.nt *= 2;
+    const int64_t tiles = (a.offsets ? (int64_t)experts + a.R / p.nt : ceil_div(a.R, p.nt)) * p.n_ct;
+    if (tiles > 0x7fffffff) return cudaErrorNotSupported;
+    const int nkb = ceil_div(a.K, kAtom * kAtoms);
+    const int64_t slots = 2 * (int64_t)num_sms;
     p.split = 1;
     while (p.split < kMaxSplit && tiles * (p.split + 1) <= slots && nkb >= p.split + 1) ++p.split;
-    int tail = 1024 + tail_bytes(p.nt, p.split, (int)E);
-    int stage = kAtoms * (kATile + p.nt * kAtom);
-    if (quantize) {
-        p.b_rows = R <= 8 ? 8 : 16;
-        p.b_atoms = (nkb + p.split - 1) / p.split * kAtoms;
-        const int64_t codes = (int64_t)p.b_atoms * p.b_rows * kAtom;
-        if (tiles > slots || per_expert > kOwnRows || codes > kCtaSmem) return false;
-        tail += (int)codes;
-        stage = kAtoms * kATile;
-    }
+    const int tail = 1024 + tail_bytes(p.nt, p.split, a.E);
+    const int stage = kAtoms * (kATile + p.nt * kAtom);
     p.stages = (kCtaSmem - tail) / stage;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
-    if (p.stages < (quantize ? 2 : 1)) return false;
+    if (p.stages < 1) return cudaErrorInvalidConfiguration;
     p.smem = tail + p.stages * stage;
     p.grid = (int)(p.split > 1 || tiles < slots ? tiles : slots) * p.split;
-    return true;
-}
 
-template <bool kQuantize>
-cudaError_t launch_planned(const W8A8Args& a, const StreamPlan& p, bool pdl, cudaStream_t stream) {
     RowMaps tx = {};
     CUtensorMap tw;
     CUresult cr = encode_tensor_map_k_atoms(&tw, a.qweight, (uint64_t)a.K, (uint64_t)a.E * (uint64_t)a.N, kCh);
-    if constexpr (!kQuantize) {
-        // one matrix: no tile has more rows than the first
-        const int most = ceil_div(ceil_div(a.R, ceil_div(a.R, p.nt)), 16) * 16;
-        for (int rows = 16; rows <= p.nt && cr == CUDA_SUCCESS; rows += 16)
-            if (a.offsets || rows <= most)
-                cr = encode_tensor_map_k_atoms(&tx.m[rows / 16 - 1], a.Xq, (uint64_t)a.K, (uint64_t)a.R, (uint32_t)rows);
-    }
+    // one matrix: no tile has more rows than the first
+    const int most = ceil_div(ceil_div(a.R, ceil_div(a.R, p.nt)), 16) * 16;
+    for (int rows = 16; rows <= p.nt && cr == CUDA_SUCCESS; rows += 16)
+        if (a.offsets || rows <= most)
+            cr = encode_tensor_map_k_atoms(&tx.m[rows / 16 - 1], a.Xq, (uint64_t)a.K, (uint64_t)a.R, (uint32_t)rows);
     if (cr != CUDA_SUCCESS) return cudaErrorInvalidValue;
-    const auto kernel = w8a8_stream_kernel<kQuantize>;
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kernel), kCtaSmem, allowed);
+    cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(w8a8_stream_kernel), kCtaSmem, allowed);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.grid);
@@ -566,26 +386,7 @@ cudaError_t launch_planned(const W8A8Args& a, const StreamPlan& p, bool pdl, cud
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, tx, tw, a, p);
-}
-
-}  // namespace
-
-cudaError_t launch_w8a8_stream(const W8A8Args& a, bool pdl, cudaStream_t stream) {
-    StreamPlan p = {};
-    if (!plan_stream(p, a.R, a.E, a.offsets != nullptr, a.N, a.K, false)) return cudaErrorNotSupported;
-    return launch_planned<false>(a, p, pdl, stream);
-}
-
-bool w8a8_rows_fit(int64_t R, int64_t E, bool grouped, int64_t N, int64_t K) {
-    StreamPlan p = {};
-    return R >= 1 && plan_stream(p, R, E, grouped, N, K, true);
-}
-
-cudaError_t launch_w8a8_rows(const W8A8Args& a, bool pdl, cudaStream_t stream) {
-    StreamPlan p = {};
-    if (!plan_stream(p, a.R, a.E, a.offsets != nullptr, a.N, a.K, true)) return cudaErrorNotSupported;
-    return launch_planned<true>(a, p, pdl, stream);
+    return cudaLaunchKernelEx(&cfg, w8a8_stream_kernel, tx, tw, a, p);
 }
 
 }  // namespace wq
