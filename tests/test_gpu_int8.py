@@ -538,6 +538,11 @@ def test_binding_refuses():
     per_group = b.quantize_w8(torch.randn(64, 128, device="cuda").to(torch.bfloat16), 32)
     bad = [
         lambda: b.linear_w8a8(x, per_group),
+        lambda: b.linear_w8a8(x, b.PackedLinearW8(p.qweight[:63], p.scales, 64, 128, 128)),
+        lambda: b.linear_w8a8(x, b.PackedLinearW8(p.qweight, p.scales.float(), 64, 128, 128)),
+        lambda: b.linear_w8a8(x, b.PackedLinearW8(p.qweight, p.scales[:60], 64, 128, 128)),
+        lambda: b.linear_w8a8(x, b.PackedLinearW8(p.qweight, p.scales.cpu(), 64, 128, 128)),
+        lambda: b.linear_w8a8_grouped(x, b.PackedExpertsW8(pe.qweight, pe.scales.float()), off),
         lambda: b.linear_w8a8(X.float(), p),
         lambda: b.linear_w8a8(X[:, :96].contiguous(), p),
         lambda: b.linear_w8a8(X.t().contiguous().t(), p),

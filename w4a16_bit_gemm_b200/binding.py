@@ -391,6 +391,14 @@ def _expect(what: str, t: torch.Tensor, dtype, shape, device):
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
+def _expect_weights(qweight, scales, rows, d_in, device):
+    """Raise unless these are the words and scales of `rows` per-channel INT8 rows."""
+    if (qweight.dtype is not torch.int32 or scales.dtype is not torch.float16 or qweight.numel() * 4 != rows * d_in
+            or scales.numel() != rows or scales.device != device or not qweight.is_contiguous()
+            or not scales.is_contiguous()):
+        raise ValueError(f"the weights must be contiguous int32 words and fp16 scales of {rows} rows on one device")
+
+
 def quantize_w8_experts(W: torch.Tensor, stream=None) -> PackedExpertsW8:
     """Per-channel INT8 quantization (quantize_w8) of bf16 W[E, d_out, d_in]."""
     _require_cuda(W)
@@ -409,7 +417,8 @@ def _token_operands(X, rows, smooth):
     """Checked (T, d_in, R) of a quantize_tokens call."""
     if X.dtype is not torch.bfloat16 or X.dim() != 2 or not X.is_contiguous():
         raise ValueError("X must be a contiguous [T, d_in] bf16 CUDA tensor")
-    _require_cuda(X)
+    if not X.is_cuda:
+        _require_cuda(X)
     T, d_in = X.shape
     R = T
     if rows is not None:
@@ -433,8 +442,8 @@ def quantize_tokens(X: torch.Tensor, rows: torch.Tensor | None = None, smooth: t
         with there:
             return quantize_tokens(X, rows, smooth, out)
     if out is None:
-        out = QuantizedTokens(torch.empty((R, d_in), dtype=torch.int8, device=device),
-                              torch.empty((R,), dtype=torch.float32, device=device))
+        out = QuantizedTokens(torch.empty_strided((R, d_in), (d_in, 1), dtype=torch.int8, device=device),
+                              torch.empty_strided((R,), (1,), dtype=torch.float32, device=device))
     else:
         _expect("out.codes", out.codes, torch.int8, (R, d_in), device)
         _expect("out.scales", out.scales, torch.float32, (R,), device)
@@ -470,7 +479,7 @@ def _w8a8_output(out, out_dtype, shape, like):
         out_dtype = out_dtype or torch.bfloat16
         if out_dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
-        out = like.new_empty(shape, dtype=out_dtype)
+        out = torch.empty_strided(shape, (shape[1], 1), dtype=out_dtype, device=like.device)
     else:
         if out.dtype not in (torch.bfloat16, torch.float32) or (out_dtype or out.dtype) != out.dtype:
             raise ValueError("out must be a bf16 or fp32 tensor (of out_dtype, when both are given)")
@@ -488,11 +497,11 @@ def linear_w8a8(x, p: PackedLinearW8, out_dtype=None, out: torch.Tensor | None =
     (q, k and v; gate and up) should quantize it once."""
     qweight, scales, d_out, d_in = p.qweight, p.scales, p.d_out, p.d_in
     device = qweight.device
-    _require_cuda(qweight)
+    if not qweight.is_cuda:
+        _require_cuda(qweight)
     if p.group_size != d_in:
         raise ValueError("linear_w8a8 takes per-channel weights (quantize_w8 without a group_size)")
-    _expect("p.qweight", qweight, torch.int32, (d_out, d_in // 4), device)
-    _expect("p.scales", scales, torch.float16, (d_out,) if scales.dim() == 1 else (d_out, 1), device)
+    _expect_weights(qweight, scales, d_out, d_in, device)
     there = _elsewhere(device, stream)
     if there is not None:
         with there:
@@ -516,9 +525,9 @@ def linear_w8a8_grouped(x, p: PackedExpertsW8, offsets: torch.Tensor, out_dtype=
     [offsets[0], offsets[E]) of the output are not written."""
     qweight, scales, E, d_out, d_in = p.qweight, p.scales, p.experts, p.d_out, p.d_in
     device = qweight.device
-    _require_cuda(qweight)
-    _expect("p.qweight", qweight, torch.int32, (E, d_out, d_in // 4), device)
-    _expect("p.scales", scales, torch.float16, (E, d_out), device)
+    if not qweight.is_cuda:
+        _require_cuda(qweight)
+    _expect_weights(qweight, scales, E * d_out, d_in, device)
     _expect("offsets", offsets, torch.int32, (E + 1,), device)
     there = _elsewhere(device, stream)
     if there is not None:
