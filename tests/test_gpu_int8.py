@@ -146,6 +146,46 @@ def test_tokens_smoothed_and_gathered(K):
     assert torch.equal(a.codes, c.codes) and torch.equal(a.scales, c.scales)
 
 
+@pytest.mark.parametrize("R,K", [(2371, 2080), (2400, 4096), (1190, 4128), (1200, 8192), (601, 11008), (700, 16384)])
+def test_tokens_smoothed_many_rows(R, K):
+    """Blocks that walk many rows: ordinary ones, zeros, non-finite and tiny ones,
+    gathered ones, smoothing scales of 0 and near the largest bf16."""
+    g = torch.Generator().manual_seed(R)
+    X = activations(R, K, 17)
+    X[5] = 0
+    X[R - 1, 3] = float("nan")
+    X[R // 2, K - 1] = float("inf")
+    X[R // 3] = X[R // 3] * 2.0 ** -110
+    smooth = (torch.rand(K, generator=g) * 4 + 0.1).to(torch.bfloat16)
+    check_tokens(X, smooth=smooth)
+    X[R - 1, 3], X[R // 2, K - 1] = 1.0, 1.0
+    rows = torch.randint(0, R, (R,), generator=g).to(torch.int32)
+    check_tokens(X, rows=rows, smooth=smooth)
+    smooth[7] = 3e38
+    check_tokens(X, smooth=smooth)
+    smooth[9] = 0.0
+    check_tokens(X, smooth=smooth)
+
+
+def test_tokens_smoothed_many_rows_with_bad_indices():
+    b = _b()
+    R, K = 3000, 4096
+    X = activations(50, K, 18)
+    rows = torch.randint(0, 50, (R,), generator=torch.Generator().manual_seed(3)).to(torch.int32)
+    rows[::11] = 50
+    rows[5::17] = -1
+    smooth = torch.full((K,), 2.0)
+    smooth[3] = 2.0 ** 127
+    smooth = smooth.to(torch.bfloat16)
+    got = b.quantize_tokens(X.cuda(), rows.cuda(), smooth.cuda())
+    _, flags = b.device_error()
+    assert flags == b.WQ_DEVFLAG_INDEX
+    q, s, _ = ref.quantize_tokens(ref.smoothed(X[rows.clamp(0, 49).long()], smooth))
+    dead = ((rows < 0) | (rows >= 50)).numpy()
+    q[dead], s[dead] = 0, 1
+    assert np.array_equal(got.codes.cpu().numpy(), q) and np.array_equal(got.scales.cpu().numpy(), s)
+
+
 def test_tokens_smoothing_at_the_ends_of_the_range():
     K = 256
     X = activations(6, K, 10).float()
