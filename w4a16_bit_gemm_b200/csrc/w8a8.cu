@@ -62,12 +62,17 @@ wq_status status_of(cudaError_t e) {
     return e == cudaSuccess ? WQ_OK : e == cudaErrorNotSupported ? WQ_ERR_UNSUPPORTED : WQ_ERR_CUDA;
 }
 
-// The product of quantized rows: up to 64 rows per matrix (on average over the
-// experts that can have any) stream the weights, more share tiles between two
-// SMs.  Measured on both sides: see the kernels.
+// The product of quantized rows.  Up to 64 rows per matrix (on average over the
+// experts that can have any) stream the weights.  More share tiles between two
+// SMs, unless the tiles are too few for half of the pairs: only the stream
+// kernel splits K.  (us, stream / pair: 64 x 8192 x 8192 20.0 / 21.0, 65 rows
+// 27.4 / 21.4; 128 x 1024 x 4096 7.0 / 10.1; 256 x 4096 x 4096 17.5 / 11.6;
+// 64 experts of 2048 x 4096 with 32 rows each 86.7 / 89.3, with 94 114 / 95.)
 cudaError_t run_product(const W8A8Args& a, int num_sms, cudaStream_t stream) {
-    const int mean = a.R / (a.E < a.R ? a.E : a.R);
-    const auto launch = mean <= 64 ? launch_w8a8_stream : launch_w8a8_pair;
+    const int64_t experts = a.E < a.R ? a.E : a.R;
+    const int64_t pair_tiles = (a.offsets ? experts + a.R / 256 : (a.R + 31) / 32) * ((a.N + 255) / 256);
+    const bool few_rows = a.R <= 64 * experts;
+    const auto launch = few_rows || pair_tiles < num_sms / 4 ? launch_w8a8_stream : launch_w8a8_pair;
     return launch(a, num_sms, pdl_enabled(), stream);
 }
 

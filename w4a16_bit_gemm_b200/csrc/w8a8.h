@@ -19,9 +19,10 @@ bool pdl_enabled();
 
 // Tensor map of an int8 matrix [rows][k] for tiles of `box_rows` rows and 128
 // bytes of k ("atoms", SWIZZLE_128B).  k a multiple of 128: coordinates (0,
-// row, atom), a load brings two atoms, one behind the other.  Else:
+// row, atom), a load brings `atoms` atoms, one behind the other.  Else:
 // coordinates (byte, row, 0), a load brings one.  Outside the matrix: zeros.
-CUresult encode_tensor_map_k_atoms(CUtensorMap* map, const void* base, uint64_t k, uint64_t rows, uint32_t box_rows);
+CUresult encode_tensor_map_k_atoms(CUtensorMap* map, const void* base, uint64_t k, uint64_t rows, int box_rows,
+                                   int atoms);
 
 cudaError_t launch_quantize_tokens(const void* X, int64_t T, int64_t K, const int32_t* rows, int64_t R,
                                    const void* smooth, int8_t* Xq, float* x_scales, uint32_t* status, bool pdl,

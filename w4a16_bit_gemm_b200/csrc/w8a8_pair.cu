@@ -333,12 +333,12 @@ cudaError_t launch_w8a8_pair(const W8A8Args& a, int num_sms, bool pdl, cudaStrea
 
     RowMaps tx = {};
     CUtensorMap tw;
-    CUresult cr = encode_tensor_map_k_atoms(&tw, a.qweight, (uint64_t)a.K, (uint64_t)a.E * (uint64_t)a.N, 128);
+    CUresult cr = encode_tensor_map_k_atoms(&tw, a.qweight, (uint64_t)a.K, (uint64_t)a.E * (uint64_t)a.N, 128, kAtoms);
     // one matrix: no tile has more rows than the first
     const int most = ceil_div(ceil_div(a.R, ceil_div(a.R, p.step)), 32) * 16;
     for (int half = 16; half <= p.step / 2 && cr == CUDA_SUCCESS; half += 16)
         if (a.offsets || half <= most)
-            cr = encode_tensor_map_k_atoms(&tx.m[half / 16 - 1], a.Xq, (uint64_t)a.K, (uint64_t)a.R, (uint32_t)half);
+            cr = encode_tensor_map_k_atoms(&tx.m[half / 16 - 1], a.Xq, (uint64_t)a.K, (uint64_t)a.R, half, kAtoms);
     if (cr != CUDA_SUCCESS) return cudaErrorInvalidValue;
     const int smem = pair_smem(a.E);
     static std::atomic<uint64_t> allowed{0};

@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kCh = 128;                  // output channels per tile (MMA M)
 constexpr int kAtom = 128;                // k per swizzle atom
-constexpr int kAtoms = 2;                 // atoms per stage
+constexpr int kMaxAtoms = 2;              // atoms per stage and copy
 constexpr int kATile = kCh * kAtom;       // bytes of weights per atom
 constexpr int kMaxRows = 64;              // rows per tile
 constexpr int kThreads = 192;             // copy warp, MMA warp, 4 epilogue warps
@@ -43,6 +43,7 @@ constexpr int kMaxSplit = 8;
 struct StreamPlan {
     int nt;       // most rows of a tile (16, 32 or 64)
     int stages;
+    int atoms;    // per stage: 2, or 1 where two stages of 2 would not fit
     int split;    // CTAs that share a tile's K
     int n_ct;     // channel tiles
     int grid;
@@ -82,8 +83,8 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int b_tile = p.nt * kAtom;
     uint8_t* smem_a = smem;
-    uint8_t* smem_b = smem + p.stages * kAtoms * kATile;
-    uint8_t* tail = smem_b + p.stages * kAtoms * b_tile;
+    uint8_t* smem_b = smem + p.stages * p.atoms * kATile;
+    uint8_t* tail = smem_b + p.stages * p.atoms * b_tile;
     uint4* recv = reinterpret_cast<uint4*>(tail);  // [sender][own group][channel]
     float* row_scale = reinterpret_cast<float*>(tail + recv_bytes(p.nt, p.split));  // [2][nt]
     int* off = reinterpret_cast<int*>(row_scale + 2 * p.nt);
@@ -94,9 +95,9 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)(blockIdx.x % (unsigned)p.split);
     const int worker = (int)(blockIdx.x / (unsigned)p.split), workers = (int)(gridDim.x / (unsigned)p.split);
-    const int atoms = (a.K + kAtom - 1) / kAtom, nkb = (atoms + kAtoms - 1) / kAtoms;
+    const int atoms = (a.K + kAtom - 1) / kAtom, nkb = (atoms + p.atoms - 1) / p.atoms;
     const int kb0 = nkb * rank / p.split, kb1 = nkb * (rank + 1) / p.split;
-    const bool whole = a.K % kAtom == 0;  // two atoms per copy
+    const bool whole = a.K % kAtom == 0;  // a stage's atoms in one copy
     const int tmem_cols = p.nt * 2;
 
     if (threadIdx.x == 0) {
@@ -140,15 +141,15 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
             const CUtensorMap* tx = &tmap_x.m[rows / 16 - 1];
             const int wrow = w.e * a.N + w.ct * kCh;
             const auto expect = [&](int s, int kb) {
-                const int here = whole ? kAtoms : min(kAtoms, atoms - kb * kAtoms);
+                const int here = whole ? p.atoms : min(p.atoms, atoms - kb * p.atoms);
                 if (one) mbar_arrive_expect_tx(&bar.full[s], (uint32_t)(here * (kATile + rows * kAtom)));
             };
             const auto load = [&](uint32_t dst, int atom_bytes, const CUtensorMap* map, int s, int kb, int row) {
                 if (whole) {
-                    tma_load_3d(one, dst, map, full0 + 8 * s, 0, row, kb * kAtoms);
+                    tma_load_3d(one, dst, map, full0 + 8 * s, 0, row, kb * p.atoms);
                 } else {
-                    for (int at = 0; at < kAtoms && kb * kAtoms + at < atoms; ++at)
-                        tma_load_3d(one, dst + at * atom_bytes, map, full0 + 8 * s, (kb * kAtoms + at) * kAtom, row, 0);
+                    for (int at = 0; at < p.atoms && kb * p.atoms + at < atoms; ++at)
+                        tma_load_3d(one, dst + at * atom_bytes, map, full0 + 8 * s, (kb * p.atoms + at) * kAtom, row, 0);
                 }
             };
             if (!waited) {
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
                 ahead = min(p.stages, kb1 - kb0);
                 for (int i = 0; i < ahead; ++i) {
                     expect(i, kb0 + i);
-                    load(a0 + i * kAtoms * kATile, kATile, &tmap_w, i, kb0 + i, wrow);
+                    load(a0 + i * p.atoms * kATile, kATile, &tmap_w, i, kb0 + i, wrow);
                 }
                 prefetch_tmap(tx);
                 pdl_wait_prior();
@@ -171,9 +172,9 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
                         break;
                     }
                     expect(s, kb);
-                    load(a0 + s * kAtoms * kATile, kATile, &tmap_w, s, kb, wrow);
+                    load(a0 + s * p.atoms * kATile, kATile, &tmap_w, s, kb, wrow);
                 }
-                load(b0 + s * kAtoms * b_tile, rows * kAtom, tx, s, kb, w.row0);
+                load(b0 + s * p.atoms * b_tile, rows * kAtom, tx, s, kb, w.row0);
             }
         }
         // the loads in flight land before the CTA ends
@@ -194,14 +195,14 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
                 tc_fence_after();
                 for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
                     const int s = it % p.stages;
-                    const uint64_t ad = sw128_kmajor_desc(smem_u32(smem_a + s * kAtoms * kATile));
-                    const uint64_t bd = sw128_kmajor_desc(smem_u32(smem_b + s * kAtoms * b_tile));
-                    const int here = min(kAtoms, atoms - kb * kAtoms);
+                    const uint64_t ad = sw128_kmajor_desc(smem_u32(smem_a + s * p.atoms * kATile));
+                    const uint64_t bd = sw128_kmajor_desc(smem_u32(smem_b + s * p.atoms * b_tile));
+                    const int here = min(p.atoms, atoms - kb * p.atoms);
                     ok = __all_sync(0xffffffffu, mbar_wait(&bar.full[s], (uint32_t)(it / p.stages) & 1u, a.status));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int at = 0; at < kAtoms; ++at) {
+                    for (int at = 0; at < kMaxAtoms; ++at) {
                         if (at >= here) break;
 #pragma unroll
                         for (int kk = 0; kk < kAtom / 32; ++kk)  // descriptors count 16-byte units
@@ -349,15 +350,17 @@ cudaError_t launch_w8a8_stream(const W8A8Args& a, int num_sms, bool pdl, cudaStr
     while (p.nt < kMaxRows && p.nt < (a.offsets ? 2 * per_expert : per_expert)) p.nt *= 2;
     const int64_t tiles = (a.offsets ? (int64_t)experts + a.R / p.nt : ceil_div(a.R, p.nt)) * p.n_ct;
     if (tiles > 0x7fffffff) return cudaErrorNotSupported;
-    const int nkb = ceil_div(a.K, kAtom * kAtoms);
+    const int atoms = ceil_div(a.K, kAtom);
     const int64_t slots = 2 * (int64_t)num_sms;
     // Clusters that all fit at once: a cluster stays within one GPC, so not every
     // slot can be used (12288 x 4096, M = 1: 288 CTAs in clusters of 3 took 16.7 us,
     // 192 in clusters of 2 take 12.6; 258 of 296 still fit).
     p.split = 1;
-    while (p.split < kMaxSplit && tiles * (p.split + 1) * 10 <= slots * 9 && nkb >= p.split + 1) ++p.split;
+    while (p.split < kMaxSplit && tiles * (p.split + 1) * 10 <= slots * 9 && atoms >= kMaxAtoms * (p.split + 1)) ++p.split;
     const int tail = 1024 + tail_bytes(p.nt, p.split, a.E);
-    const int stage = kAtoms * (kATile + p.nt * kAtom);
+    p.atoms = kMaxAtoms;
+    if ((kCtaSmem - tail) / (p.atoms * (kATile + p.nt * kAtom)) < 2) p.atoms = 1;
+    const int stage = p.atoms * (kATile + p.nt * kAtom);
     p.stages = (kCtaSmem - tail) / stage;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     if (p.stages < 1) return cudaErrorInvalidConfiguration;
@@ -366,12 +369,12 @@ cudaError_t launch_w8a8_stream(const W8A8Args& a, int num_sms, bool pdl, cudaStr
 
     RowMaps tx = {};
     CUtensorMap tw;
-    CUresult cr = encode_tensor_map_k_atoms(&tw, a.qweight, (uint64_t)a.K, (uint64_t)a.E * (uint64_t)a.N, kCh);
+    CUresult cr = encode_tensor_map_k_atoms(&tw, a.qweight, (uint64_t)a.K, (uint64_t)a.E * (uint64_t)a.N, kCh, p.atoms);
     // one matrix: no tile has more rows than the first
     const int most = ceil_div(ceil_div(a.R, ceil_div(a.R, p.nt)), 16) * 16;
     for (int rows = 16; rows <= p.nt && cr == CUDA_SUCCESS; rows += 16)
         if (a.offsets || rows <= most)
-            cr = encode_tensor_map_k_atoms(&tx.m[rows / 16 - 1], a.Xq, (uint64_t)a.K, (uint64_t)a.R, (uint32_t)rows);
+            cr = encode_tensor_map_k_atoms(&tx.m[rows / 16 - 1], a.Xq, (uint64_t)a.K, (uint64_t)a.R, rows, p.atoms);
     if (cr != CUDA_SUCCESS) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(w8a8_stream_kernel), kCtaSmem, allowed);

@@ -189,13 +189,14 @@ CUresult encode_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const
                     swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-CUresult encode_tensor_map_k_atoms(CUtensorMap* map, const void* base, uint64_t k, uint64_t rows, uint32_t box_rows) {
+CUresult encode_tensor_map_k_atoms(CUtensorMap* map, const void* base, uint64_t k, uint64_t rows, int box_rows,
+                                   int atoms) {
     CUresult cr = encoder_ready();
     if (cr != CUDA_SUCCESS) return cr;
     const bool whole = k % 128 == 0;
     cuuint64_t dims[3] = {whole ? 128 : k, rows, whole ? k / 128 : 1};
     cuuint64_t strides[2] = {k, 128};
-    cuuint32_t box[3] = {128, box_rows, whole ? 2u : 1u};
+    cuuint32_t box[3] = {128, (cuuint32_t)box_rows, whole ? (cuuint32_t)atoms : 1u};
     cuuint32_t estr[3] = {1, 1, 1};
     return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
