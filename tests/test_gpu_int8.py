@@ -247,7 +247,9 @@ def test_linear_few_tokens(M, N, K):
 
 @pytest.mark.parametrize("M,N,K", [(127, 300, 160), (128, 640, 512), (129, 257, 1056), (255, 128, 96), (256, 1000, 288),
                                    (257, 255, 2080), (300, 1001, 1056), (513, 600, 128), (777, 1409, 544),
-                                   (1030, 2049, 1024), (2500, 513, 256)])
+                                   (1030, 2049, 1024), (2500, 513, 256),
+                                   # deep and narrow: the stream kernel with several token tiles and K split
+                                   (65, 200, 4096), (129, 300, 4100 // 32 * 32), (250, 520, 8192), (511, 130, 2080)])
 def test_linear_many_tokens(M, N, K):
     check_linear(M, N, K, M, torch.float32 if N % 2 else torch.bfloat16)
 

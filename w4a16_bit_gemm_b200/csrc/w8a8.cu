@@ -63,16 +63,20 @@ wq_status status_of(cudaError_t e) {
 }
 
 // The product of quantized rows.  Up to 64 rows per matrix (on average over the
-// experts that can have any) stream the weights.  More share tiles between two
-// SMs, unless the tiles are too few for half of the pairs: only the stream
-// kernel splits K.  (us, stream / pair: 64 x 8192 x 8192 20.0 / 21.0, 65 rows
-// 27.4 / 21.4; 128 x 1024 x 4096 7.0 / 10.1; 256 x 4096 x 4096 17.5 / 11.6;
-// 64 experts of 2048 x 4096 with 32 rows each 86.7 / 89.3, with 94 114 / 95.)
+// experts that can have any) stream the weights; more share tiles between two
+// SMs.  Where the pairs' tiles do not give every pair one, a deep product
+// streams all the same: only that kernel splits K.  Measured, us stream / pair:
+//   64 x 8192 x 8192 18.3 / 21.0   128 x 4096 x 11008 17.2 / 23.8   256 x 2048 x 8192 13.1 / 17.5
+//   96 x 8192 x 8192 22.2 / 21.4   160 x 4096 x 4096 13.4 / 11.6    128 x 1001 x 1056 5.5 / 5.0
+//   64 experts of 2048 x 4096, 64 rows each 92.6 / 92.3, 94 rows 116 / 95
+//   2 experts, 150 rows, 512 x 4096 8.2 / 10.8; 160 rows, 4096 x 4096 16.2 / 15.0
 cudaError_t run_product(const W8A8Args& a, int num_sms, cudaStream_t stream) {
     const int64_t experts = a.E < a.R ? a.E : a.R;
-    const int64_t pair_tiles = (a.offsets ? experts + a.R / 256 : (a.R + 31) / 32) * ((a.N + 255) / 256);
-    const bool few_rows = a.R <= 64 * experts;
-    const auto launch = few_rows || pair_tiles < num_sms / 4 ? launch_w8a8_stream : launch_w8a8_pair;
+    const int pairs = num_sms / 2;
+    const int64_t n_ct = (a.N + 255) / 256;
+    const bool few_tiles = a.offsets ? (experts + a.R / 256) * n_ct < pairs / 4 : (a.R + 31) / 32 * n_ct < pairs;
+    const bool streams = a.R <= 64 * experts || (few_tiles && a.K >= 2048);
+    const auto launch = streams ? launch_w8a8_stream : launch_w8a8_pair;
     return launch(a, num_sms, pdl_enabled(), stream);
 }
 
