@@ -163,7 +163,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
         tc_fence_before();
     }
-    pdl_wait_prior();
+    if (a.offsets) pdl_wait_prior();
     build_tiles(a.offsets, a.E, a.R, p.step, off, cum, warp_part, kThreads, a.status);  // ends with __syncthreads
     cluster_arrive();
     cluster_wait();  // both CTAs' barriers are initialised
@@ -177,33 +177,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool one = elect_one();
         const uint32_t a0 = smem_u32(smem_a), b0 = smem_u32(smem_b);
         const uint32_t full0 = map_rank(smem_u32(bar.full), 0);  // the leader's
-        int it = 0;
+        int it = 0, ahead = 0;
+        bool waited = a.offsets != nullptr;
         for (int t = worker; t < total && !__any_sync(0xffffffffu, *abort_flag); t += workers) {
             const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
             const int half = ceil_div(w.n, 32) * 16;  // rows this CTA brings
             const int wrow = w.e * a.N + w.ct * kCh + rank * 128;
             const int xrow = w.row0 + rank * half;
             const CUtensorMap* tx = &tmap_x.m[half / 16 - 1];
-            for (int kb = 0; kb < nkb; ++kb, ++it) {
-                const int s = it % kStages;
-                if (it >= kStages &&
-                    !__all_sync(0xffffffffu, mbar_wait(&bar.empty[s], (uint32_t)(it / kStages - 1) & 1u, a.status))) {
-                    atomicExch(&bar.abort_flag, 1);
-                    break;
-                }
+            const auto expect = [&](int s, int kb) {
                 const int here = whole ? kAtoms : min(kAtoms, atoms - kb * kAtoms);
                 if (rank == 0 && one) mbar_arrive_expect_tx(&bar.full[s], (uint32_t)(2 * here * (kATile + half * kKB)));
-                const uint32_t full = full0 + 8 * s, as = a0 + s * kAtoms * kATile, bs = b0 + s * kAtoms * kBTile;
+            };
+            const auto load = [&](uint32_t dst, int atom_bytes, const CUtensorMap* map, int s, int kb, int row) {
                 if (whole) {
-                    tma_load_3d_pair(one, as, &tmap_w, full, 0, wrow, kb * kAtoms);
-                    tma_load_3d_pair(one, bs, tx, full, 0, xrow, kb * kAtoms);
+                    tma_load_3d_pair(one, dst, map, full0 + 8 * s, 0, row, kb * kAtoms);
                 } else {
-                    for (int at = 0; at < here; ++at) {
-                        const int x = (kb * kAtoms + at) * kKB;
-                        tma_load_3d_pair(one, as + at * kATile, &tmap_w, full, x, wrow, 0);
-                        tma_load_3d_pair(one, bs + at * half * kKB, tx, full, x, xrow, 0);
-                    }
+                    for (int at = 0; at < kAtoms && kb * kAtoms + at < atoms; ++at)
+                        tma_load_3d_pair(one, dst + at * atom_bytes, map, full0 + 8 * s, (kb * kAtoms + at) * kKB, row, 0);
                 }
+            };
+            if (!waited) {
+                // one weight matrix: what does not depend on the previous kernel goes first
+                ahead = min(kStages, nkb);
+                for (int i = 0; i < ahead; ++i) {
+                    expect(i, i);
+                    load(a0 + i * kAtoms * kATile, kATile, &tmap_w, i, i, wrow);
+                }
+                prefetch_tmap(tx);
+                pdl_wait_prior();
+                waited = true;
+            }
+            for (int kb = 0; kb < nkb; ++kb, ++it) {
+                const int s = it % kStages;
+                if (it >= ahead) {
+                    if (it >= kStages &&
+                        !__all_sync(0xffffffffu, mbar_wait(&bar.empty[s], (uint32_t)(it / kStages - 1) & 1u, a.status))) {
+                        atomicExch(&bar.abort_flag, 1);
+                        break;
+                    }
+                    expect(s, kb);
+                    load(a0 + s * kAtoms * kATile, kATile, &tmap_w, s, kb, wrow);
+                }
+                load(b0 + s * kAtoms * kBTile, half * kKB, tx, s, kb, xrow);
             }
         }
         // before the pair ends, the loads in flight (of both CTAs) land in the
@@ -261,6 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int q = warp & 3;            // tensor memory lanes this warp may read
         const int ch = rank * 128 + q * 32 + lane;
         const int et = threadIdx.x - 64;
+        if (!a.offsets) pdl_wait_prior();
         const int part = (warp - 2) >> 2;  // which half of the 64-column groups
         int ti = 0;
         for (int t = worker; t < total; t += workers, ++ti) {
