@@ -55,7 +55,7 @@ extern "C" {
  *   d_in         a multiple of 32, 32 .. WQ_INT8_MAX_D_IN.
  *   rows         device int32 [R] or NULL.  Output row r quantizes X row
  *                rows[r] (a token sent to several experts is quantized into
- *                each expert's rows).  NULL: R must equal T, row r is X row r.
+ *                each expert's rows).  NULL: R must equal T (or be 0), row r is X row r.
  *                An index outside [0, T) gives a row of zero codes with scale
  *                1 and raises WQ_DEVFLAG_INDEX.
  *   R            output rows, 0 .. 2^31 - 1; 0 enqueues nothing (the arrays
@@ -89,13 +89,13 @@ wq_status wq_quantize_tokens(const void* X_bf16, int64_t T, int64_t d_in, const 
  *   d_out        1 .. 2^31 - 1.
  *   d_in         a multiple of 32, 32 .. WQ_INT8_MAX_D_IN.
  *   Y            [M][d_out] output, y_dtype as wq_linear_w4a16.  16-byte aligned.
- * A call may read qweight (and the tensor maps' memory behind it) before the
- * kernel ahead of it on the stream has ended, if that kernel allows its
- * successor to start early (programmatic dependent launch: this library's
- * linear layers and wq_quantize_tokens do; none of them writes weights).
+ * A call may read qweight and scales_fp16 before the kernel ahead of it on the
+ * stream has ended, if that kernel allows its successor to start early
+ * (programmatic dependent launch: this library's linear layers and
+ * wq_quantize_tokens do; none of them writes weights).
  * Everything else is read, and Y written, after the work ahead has ended.
  * Errors: WQ_ERR_INVALID_ARG as above; WQ_ERR_UNSUPPORTED for a product of
- * more than 2^31 - 1 output tiles; WQ_ERR_CUDA if a launch fails.
+ * more than 2^30 output tiles; WQ_ERR_CUDA if a launch fails.
  * Device flags: WQ_DEVFLAG_TIMEOUT if a pipeline wait inside the kernel gave
  * up (the output is then incomplete).
  */

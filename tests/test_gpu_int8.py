@@ -229,6 +229,16 @@ def test_tokens_bad_row_index_is_flagged_and_coded_zero():
     assert np.array_equal(got.codes.cpu().numpy(), q) and np.array_equal(got.scales.cpu().numpy(), s)
 
 
+def test_tokens_none_to_gather_from():
+    b = _b()
+    rows = torch.zeros(3, dtype=torch.int32, device="cuda")
+    got = b.quantize_tokens(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), rows)
+    _, flags = b.device_error()
+    assert flags == b.WQ_DEVFLAG_INDEX and not got.codes.any() and torch.equal(got.scales, torch.ones_like(got.scales))
+    none = b.quantize_tokens(torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda"), rows[:0])
+    assert none.codes.shape == (0, 64) and none.scales.shape == (0,)
+
+
 # ---------------------------------------------------------------------------
 # linear_w8a8
 # ---------------------------------------------------------------------------
@@ -550,6 +560,27 @@ def test_back_to_back_launches_keep_their_order():
             torch.cuda.synchronize()
             cur = b.linear_w8a8(cur, p).clone()
         assert torch.equal(cur, first)
+
+
+def test_mixed_with_the_other_linear_layers():
+    """Kernels that start early beside each other and share tensor memory: 4-bit
+    and 8-bit layers of every path in one stream, many times over."""
+    b = _b()
+    g = torch.Generator().manual_seed(8)
+    W = (torch.randn(2048, 2048, generator=g) * 0.03).to(torch.bfloat16).cuda()
+    p4, p8 = b.quantize_rtn(W, 128, True), b.quantize_w8(W)
+    for M in (1, 2, 8, 16, 40, 200):
+        x = torch.randn(M, 2048, generator=g).to(torch.bfloat16).cuda()
+        first = None
+        for _ in range(15):
+            cur = x
+            for _ in range(3):
+                cur = b.linear_w8a8(cur, p8)
+                cur = b.linear_w4a16(cur, p4)
+                cur = b.linear_w8a8(b.quantize_tokens(cur), p8)
+                cur = b.linear_w8a16(cur, p8)
+            first = cur.clone() if first is None else first
+            assert torch.equal(cur, first)
 
 
 def test_two_streams_at_once():

@@ -32,7 +32,7 @@ wq_status check_codes(const int8_t* Xq, const float* x_scales, int64_t rows) {
 
 wq_status check_tokens(const void* X, int64_t T, int64_t d_in, const int32_t* rows, int64_t R, const void* smooth) {
     if (T < 0 || T > kMaxInt32 || R < 0 || R > kMaxInt32 || !depth_ok(d_in)) return WQ_ERR_INVALID_ARG;
-    if (!rows && R != T) return WQ_ERR_INVALID_ARG;
+    if (!rows && R != T && R != 0) return WQ_ERR_INVALID_ARG;
     if (R > 0 && T > 0 && !X) return WQ_ERR_INVALID_ARG;
     return aligned(X, 16) && aligned(rows, 4) && aligned(smooth, 2) ? WQ_OK : WQ_ERR_INVALID_ARG;
 }

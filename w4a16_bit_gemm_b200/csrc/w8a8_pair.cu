@@ -141,7 +141,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int atoms = (a.K + kKB - 1) / kKB, nkb = (atoms + kAtoms - 1) / kAtoms;
     const bool whole = a.K % kKB == 0;  // two atoms per copy
 
-    pdl_launch_dependents();
     if (threadIdx.x == 0) {
         prefetch_tmap(&tmap_w);
         for (int s = 0; s < kStages; ++s) {
@@ -165,6 +164,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (a.offsets) pdl_wait_prior();
     build_tiles(a.offsets, a.E, a.R, p.step, off, cum, warp_part, kThreads, a.status);  // ends with __syncthreads
+    // Only now may the next kernel start: it could take the tensor memory that
+    // this one still has to allocate, and wait for it.
+    pdl_launch_dependents();
     cluster_arrive();
     cluster_wait();  // both CTAs' barriers are initialised
     tc_fence_after();
@@ -234,6 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ---------------- MMA warp (leader) ----------------
+        if (!a.offsets) pdl_wait_prior();  // the bounded waits below do not cover the previous kernel
         if (rank == 0) {
             const bool one = elect_one();
             int it = 0, ti = 0;
@@ -346,7 +349,7 @@ cudaError_t launch_w8a8_pair(const W8A8Args& a, int num_sms, bool pdl, cudaStrea
     }
     const int64_t token_tiles = a.offsets ? (int64_t)(a.E < a.R ? a.E : a.R) + a.R / p.step : ceil_div(a.R, p.step);
     const int64_t tiles = token_tiles * p.n_ct;
-    if (tiles > 0x7fffffff) return cudaErrorNotSupported;
+    if (tiles > 0x3fffffff) return cudaErrorNotSupported;  // tile numbers stay far from overflow
 
     RowMaps tx = {};
     CUtensorMap tw;

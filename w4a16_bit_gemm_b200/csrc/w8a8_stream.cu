@@ -115,7 +115,6 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
         bar.abort_flag = 0;
         fence_mbar_init();
     }
-    pdl_launch_dependents();
     if (warp == 1) {
         tmem_alloc(&bar.tmem_slot, (uint32_t)tmem_cols);
         tmem_relinquish();
@@ -123,6 +122,9 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
     }
     if (a.offsets) pdl_wait_prior();
     build_tiles(a.offsets, a.E, a.R, p.nt, off, cum, warp_part, kThreads, a.status);  // ends with __syncthreads
+    // Only now may the next kernel start: it could take the tensor memory that
+    // this one still has to allocate, and wait for it.
+    pdl_launch_dependents();
     if (p.split > 1) cluster_arrive();
     tc_fence_after();
     const uint32_t tmem_base = bar.tmem_slot;
@@ -183,44 +185,43 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
         __syncwarp();
     } else if (warp == 1) {
         // ---------------- MMA warp ----------------
-        {
-            const bool one = elect_one();
-            int it = 0, ti = 0;
-            for (int t = worker; t < total && !__any_sync(0xffffffffu, *abort_flag); t += workers, ++ti) {
-                const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 16);
-                const int rows = (w.n + 15) & ~15;
-                const uint32_t idesc = mma_idesc_s8(kCh, rows);
-                const int acc = ti & 1;
-                bool ok = ti < 2 || __all_sync(0xffffffffu, mbar_wait(&bar.acc_empty[acc], (uint32_t)((ti >> 1) - 1) & 1u, a.status));
+        if (!a.offsets) pdl_wait_prior();  // the bounded waits below do not cover the previous kernel
+        const bool one = elect_one();
+        int it = 0, ti = 0;
+        for (int t = worker; t < total && !__any_sync(0xffffffffu, *abort_flag); t += workers, ++ti) {
+            const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 16);
+            const int rows = (w.n + 15) & ~15;
+            const uint32_t idesc = mma_idesc_s8(kCh, rows);
+            const int acc = ti & 1;
+            bool ok = ti < 2 || __all_sync(0xffffffffu, mbar_wait(&bar.acc_empty[acc], (uint32_t)((ti >> 1) - 1) & 1u, a.status));
+            tc_fence_after();
+            for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
+                const int s = it % p.stages;
+                const uint64_t ad = sw128_kmajor_desc(smem_u32(smem_a + s * p.atoms * kATile));
+                const uint64_t bd = sw128_kmajor_desc(smem_u32(smem_b + s * p.atoms * b_tile));
+                const int here = min(p.atoms, atoms - kb * p.atoms);
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar.full[s], (uint32_t)(it / p.stages) & 1u, a.status));
+                if (!ok) break;
                 tc_fence_after();
-                for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
-                    const int s = it % p.stages;
-                    const uint64_t ad = sw128_kmajor_desc(smem_u32(smem_a + s * p.atoms * kATile));
-                    const uint64_t bd = sw128_kmajor_desc(smem_u32(smem_b + s * p.atoms * b_tile));
-                    const int here = min(p.atoms, atoms - kb * p.atoms);
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bar.full[s], (uint32_t)(it / p.stages) & 1u, a.status));
-                    if (!ok) break;
-                    tc_fence_after();
 #pragma unroll
-                    for (int at = 0; at < kMaxAtoms; ++at) {
-                        if (at >= here) break;
+                for (int at = 0; at < kMaxAtoms; ++at) {
+                    if (at >= here) break;
 #pragma unroll
-                        for (int kk = 0; kk < kAtom / 32; ++kk)  // descriptors count 16-byte units
-                            tc_mma_i8(one, tmem_base + (uint32_t)(acc * p.nt), ad + (at * kATile + kk * 32) / 16,
-                                      bd + (at * rows * kAtom + kk * 32) / 16, idesc,
-                                      (kb != kb0 || at != 0 || kk != 0) ? 1u : 0u);
-                    }
-                    if (one) tc_commit(&bar.empty[s]);
+                    for (int kk = 0; kk < kAtom / 32; ++kk)  // descriptors count 16-byte units
+                        tc_mma_i8(one, tmem_base + (uint32_t)(acc * p.nt), ad + (at * kATile + kk * 32) / 16,
+                                  bd + (at * rows * kAtom + kk * 32) / 16, idesc,
+                                  (kb != kb0 || at != 0 || kk != 0) ? 1u : 0u);
                 }
-                if (!ok) {
-                    atomicExch(&bar.abort_flag, 1);
-                    break;
-                }
-                if (one) tc_commit(&bar.acc_full[acc]);
+                if (one) tc_commit(&bar.empty[s]);
             }
-            if (one) tc_commit(&bar.drain);  // completes once every MMA issued above has
-            mbar_wait(&bar.drain, 0u, a.status);
+            if (!ok) {
+                atomicExch(&bar.abort_flag, 1);
+                break;
+            }
+            if (one) tc_commit(&bar.acc_full[acc]);
         }
+        if (one) tc_commit(&bar.drain);  // completes once every MMA issued above has
+        mbar_wait(&bar.drain, 0u, a.status);
         __syncwarp();
     } else {
         // ---------------- epilogue warps ----------------
@@ -349,7 +350,7 @@ cudaError_t launch_w8a8_stream(const W8A8Args& a, int num_sms, bool pdl, cudaStr
     p.nt = 16;
     while (p.nt < kMaxRows && p.nt < (a.offsets ? 2 * per_expert : per_expert)) p.nt *= 2;
     const int64_t tiles = (a.offsets ? (int64_t)experts + a.R / p.nt : ceil_div(a.R, p.nt)) * p.n_ct;
-    if (tiles > 0x7fffffff) return cudaErrorNotSupported;
+    if (tiles > 0x3fffffff) return cudaErrorNotSupported;  // tile numbers stay far from overflow
     const int atoms = ceil_div(a.K, kAtom);
     const int64_t slots = 2 * (int64_t)num_sms;
     // Clusters that all fit at once: a cluster stays within one GPC, so not every
