@@ -22,6 +22,14 @@
 // it, the activations do.  What follows the wait is kept short: one load of
 // the rows, the MMAs, one exchange.  Every wait is bounded
 // (WQ_DEVFLAG_TIMEOUT).
+//
+// Measured (weights from HBM, launches back to back): 4096 x 4096 5.75 us for
+// 1 row, 6.1 for 16, 8.3 for 64; 11008 x 4096, 16 rows 11.7 us (3.9 TB/s);
+// 28672 x 8192, 1 row 39 us (6.0 TB/s, 91 % of the measured copy rate); 64
+// experts of 2048 x 4096, 2 rows each 84 us (97 %).  Beyond the stream itself a
+// call costs about 3 us (one matrix) to 6 us (experts: the offsets come first).
+// Codes made inside this kernel in place of a quantizer launch were slower
+// (7.4 us and more against 6.6 for both launches, 4096 x 4096, 1 row).
 #include <stdint.h>
 
 #include "w8a8.h"
