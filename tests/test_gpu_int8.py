@@ -474,6 +474,67 @@ def test_grouped_equals_dense_per_expert():
 
 
 # ---------------------------------------------------------------------------
+# Offsets beyond 32 bits: activations, codes, weights and outputs of more than
+# 2^31 elements, checked on rows at both ends and around the border
+# ---------------------------------------------------------------------------
+
+def _codes(g, *shape):
+    return torch.randint(-127, 128, shape, generator=g, device="cuda", dtype=torch.int8)
+
+
+def test_more_than_2_31_activations():
+    b = _b()
+    R, K, N = 266_000, 8192, 130
+    g = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.randn(R, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    x = b.quantize_tokens(X)
+    at = torch.tensor([0, 1, 131071, 131072, 262143, 262144, R - 2, R - 1], device="cuda")
+    q, s, _ = ref.quantize_tokens(X[at].cpu())
+    assert np.array_equal(x.codes[at].cpu().numpy(), q) and np.array_equal(x.scales[at].cpu().numpy(), s)
+    del X
+    wq, ws = _codes(g, N, K), torch.rand(N, generator=g, device="cuda").half()
+    Y = b.linear_w8a8(x, b.PackedLinearW8(wq.view(torch.int32), ws, N, K, K), out_dtype=torch.float32)
+    y, y64 = ref.product(q, s, wq.cpu().numpy(), ws.cpu().numpy())
+    ref.check(Y[at], y, y64)
+
+
+def test_more_than_2_31_outputs():
+    b = _b()
+    M, N, K = 76_000, 28672, 64
+    g = torch.Generator(device="cuda").manual_seed(2)
+    xq, xs = _codes(g, M, K), torch.rand(M, generator=g, device="cuda")
+    wq, ws = _codes(g, N, K), torch.rand(N, generator=g, device="cuda").half()
+    p = b.PackedLinearW8(wq.view(torch.int32), ws, N, K, K)
+    at = torch.tensor([0, 37449, 74898, 74899, M - 1], device="cuda")
+    y, y64 = ref.product(xq[at].cpu().numpy(), xs[at].cpu().numpy(), wq.cpu().numpy(), ws.cpu().numpy())
+    ref.check(b.linear_w8a8(b.QuantizedTokens(xq, xs), p)[at], y, y64)
+    # a few rows per expert: the stream kernel's stores
+    pe = b.PackedExpertsW8(wq.view(torch.int32).expand(2, N, K // 4).contiguous(), ws.expand(2, N).contiguous())
+    off = torch.tensor([M - 40, M - 20, M], dtype=torch.int32, device="cuda")
+    held = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    got = b.linear_w8a8_grouped(b.QuantizedTokens(xq, xs), pe, off, out=held)
+    ref.check(got[at[-1:]], y[-1:], y64[-1:])
+    assert not got[:M - 40].any()
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_more_than_2_31_weights(rows):
+    b = _b()
+    E, N, K = 50, 11008, 4096
+    g = torch.Generator(device="cuda").manual_seed(3)
+    wq, ws = _codes(g, E, N, K), torch.rand(E, N, generator=g, device="cuda").half()
+    xq, xs = _codes(g, 2 * rows, K), torch.rand(2 * rows, generator=g, device="cuda")
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[48:] = rows        # expert 47 (its weights straddle 2^31 bytes) and the last one
+    off[E:] = 2 * rows
+    got = b.linear_w8a8_grouped(b.QuantizedTokens(xq, xs), b.PackedExpertsW8(wq.view(torch.int32), ws), off)
+    for e, lo in ((47, 0), (E - 1, rows)):
+        y, y64 = ref.product(xq[lo:lo + rows].cpu().numpy(), xs[lo:lo + rows].cpu().numpy(), wq[e].cpu().numpy(),
+                             ws[e].cpu().numpy())
+        ref.check(got[lo:lo + rows], y, y64)
+
+
+# ---------------------------------------------------------------------------
 # Used together, streams, graphs
 # ---------------------------------------------------------------------------
 

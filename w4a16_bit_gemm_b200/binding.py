@@ -367,6 +367,9 @@ class PackedExpertsW8:
         return self.qweight.numel() * 4 + self.scales.numel() * 2
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _elsewhere(device, stream):
     """None when a call for tensors on `device` can be queued as things stand:
     the device is the current one and no stream is named.  Otherwise a context
@@ -375,7 +378,7 @@ def _elsewhere(device, stream):
         if stream.device != device:
             raise ValueError("stream and tensors are on different devices")
         return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
+    if device.index != _current_device():
         return torch.cuda.device(device)
     return None
 
