@@ -258,6 +258,8 @@ def test_linear_few_tokens(M, N, K):
 @pytest.mark.parametrize("M,N,K", [(127, 300, 160), (128, 640, 512), (129, 257, 1056), (255, 128, 96), (256, 1000, 288),
                                    (257, 255, 2080), (300, 1001, 1056), (513, 600, 128), (777, 1409, 544),
                                    (1030, 2049, 1024), (2500, 513, 256),
+                                   # deep: tiles of 512 channels, whole and ragged ones
+                                   (1100, 1000, 8192), (2100, 513, 8224), (700, 2050, 11008),
                                    # deep and narrow: the stream kernel with several token tiles and K split
                                    (65, 200, 4096), (129, 300, 4100 // 32 * 32), (250, 520, 8192), (511, 130, 2080)])
 def test_linear_many_tokens(M, N, K):

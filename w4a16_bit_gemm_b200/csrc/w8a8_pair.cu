@@ -10,7 +10,9 @@
 // Rows are the N side, so a tile with few rows (the last one of a prompt, a
 // lightly loaded expert) costs its own rows rounded up to 32, not a full tile.
 // The accumulator is int32 in tensor memory, two of 256 columns: the epilogue
-// of a tile runs under the products of the next.  Persistent: each pair walks
+// of a tile runs under the products of the next.  Or both belong to one tile of
+// 512 channels, which reads a quarter less from L2 (13 to 14 TB/s into the SMs
+// was the bound of 256-channel tiles at full clock).  Persistent: each pair walks
 // the tiles in steps of the number of pairs.  Every wait is bounded
 // (WQ_DEVFLAG_TIMEOUT).
 //
@@ -30,16 +32,26 @@
 namespace wq {
 namespace {
 
-constexpr int kCh = 256;                 // output channels per tile, 128 per CTA
 constexpr int kKB = 128;                 // k per swizzle atom
-constexpr int kAtoms = 2;                // atoms per stage
 constexpr int kMaxRows = 256;            // rows per tile
-constexpr int kATile = 128 * kKB;        // bytes per CTA and stage
-constexpr int kBTile = 128 * kKB;
-constexpr int kStages = 3;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;  // copy warp, MMA warp, epilogue warps
+constexpr int kBTile = 128 * kKB;        // bytes of rows per CTA and atom
+constexpr int kEpiWarps = 8;             // per accumulator of a tile
 constexpr int kTmemCols = 2 * kMaxRows;
+
+// kSub = 1: tiles of 256 channels, 128 per CTA; the two accumulators belong to
+// successive tiles.  kSub = 2: tiles of 512 channels, 256 per CTA; each
+// accumulator takes 128 of them, and a row is fetched once for both.
+template <int kSub>
+struct Shape {
+    static constexpr int kCh = 256 * kSub;           // channels per tile
+    static constexpr int kCtaCh = 128 * kSub;        // channels per CTA
+    static constexpr int kAtoms = kSub == 1 ? 2 : 1; // atoms per stage
+    static constexpr int kStages = kSub == 1 ? 3 : 4;
+    static constexpr int kATile = kCtaCh * kKB;      // bytes of weights per CTA and atom
+    static constexpr int kEpi = 32 * kEpiWarps * kSub;  // epilogue threads
+    static constexpr int kThreads = 64 + kEpi;       // copy warp, MMA warp, epilogue warps
+};
+constexpr int kMostStages = 4;
 
 struct PairPlan {
     int step;   // most rows of a tile, a multiple of 32
@@ -53,8 +65,8 @@ struct RowMaps {
 };
 
 struct PairBars {
-    uint64_t full[kStages];   // leader: both CTAs' bytes
-    uint64_t empty[kStages];
+    uint64_t full[kMostStages];   // leader: both CTAs' bytes
+    uint64_t empty[kMostStages];
     uint64_t acc_full[2];
     uint64_t acc_empty[2];    // leader: the epilogue warps of both CTAs
     uint64_t drain;           // leader
@@ -63,10 +75,14 @@ struct PairBars {
 };
 
 __host__ __device__ constexpr int table_ints(int E) { return (E + 1 + 3) & ~3; }
+template <int kSub>
 __host__ __device__ constexpr int pair_smem(int E) {
-    return 1024 + kStages * kAtoms * (kATile + kBTile) + 2 * kMaxRows * 4 + 2 * table_ints(E) * 4 + 64 * 4 + (int)sizeof(PairBars);
+    using S = Shape<kSub>;
+    return 1024 + S::kStages * S::kAtoms * (S::kATile + kBTile) + 2 * kMaxRows * 4 + 2 * table_ints(E) * 4 + 64 * 4 +
+           (int)sizeof(PairBars);
 }
-static_assert(pair_smem(WQ_INT8_MAX_EXPERTS) <= 227 * 1024, "pair kernel shared memory");
+static_assert(pair_smem<1>(WQ_INT8_MAX_EXPERTS) <= 227 * 1024 && pair_smem<2>(WQ_INT8_MAX_EXPERTS) <= 227 * 1024,
+              "pair kernel shared memory");
 
 __device__ __forceinline__ void tc_mma_i8_pair(bool one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                uint32_t accumulate) {
@@ -128,9 +144,12 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     }
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <int kSub>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub>::kThreads, 1)
     w8a8_pair_kernel(const __grid_constant__ RowMaps tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                      const W8A8Args a, const PairPlan p) {
+    using S = Shape<kSub>;
+    constexpr int kCh = S::kCh, kAtoms = S::kAtoms, kStages = S::kStages, kATile = S::kATile;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* smem_a = smem;
@@ -169,7 +188,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
     }
     if (a.offsets) pdl_wait_prior();
-    build_tiles(a.offsets, a.E, a.R, p.step, off, cum, warp_part, kThreads, a.status);  // ends with __syncthreads
+    build_tiles(a.offsets, a.E, a.R, p.step, off, cum, warp_part, S::kThreads, a.status);  // ends with __syncthreads
     // Only now may the next kernel start: it could take the tensor memory that
     // this one still has to allocate, and wait for it.
     pdl_launch_dependents();
@@ -190,7 +209,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int t = worker; t < total && !__any_sync(0xffffffffu, *abort_flag); t += workers) {
             const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
             const int half = ceil_div(w.n, 32) * 16;  // rows this CTA brings
-            const int wrow = w.e * a.N + w.ct * kCh + rank * 128;
+            const int wrow = w.e * a.N + w.ct * kCh + rank * S::kCtaCh;
             const int xrow = w.row0 + rank * half;
             const CUtensorMap* tx = &tmap_x.m[half / 16 - 1];
             const auto expect = [&](int s, int kb) {
@@ -249,33 +268,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int t = worker; t < total && !__any_sync(0xffffffffu, *abort_flag); t += workers, ++ti) {
                 const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
                 const int half = ceil_div(w.n, 32) * 16;
-                const uint32_t idesc = mma_idesc_s8(kCh, 2 * half);
-                const int acc = ti & 1;
-                bool ok = ti < 2 || __all_sync(0xffffffffu, mbar_wait_cluster(&bar.acc_empty[acc], (uint32_t)((ti >> 1) - 1) & 1u, a.status));
-                tc_fence_after();
+                const uint32_t idesc = mma_idesc_s8(256, 2 * half);
+                // accumulator of the tile's (sub)tile j, and how often it was used before
+                const auto acc_of = [&](int j) { return kSub == 1 ? ti & 1 : j; };
+                const int uses = kSub == 1 ? ti >> 1 : ti;
+                bool ok = true;
                 for (int kb = 0; ok && kb < nkb; ++kb, ++it) {
                     const int s = it % kStages;
                     ok = __all_sync(0xffffffffu, mbar_wait(&bar.full[s], (uint32_t)(it / kStages) & 1u, a.status));
-                    if (!ok) break;
-                    tc_fence_after();
                     const uint64_t ad = sw128_kmajor_desc(smem_u32(smem_a + s * kAtoms * kATile));
                     const uint64_t bd = sw128_kmajor_desc(smem_u32(smem_b + s * kAtoms * kBTile));
                     const int here = min(kAtoms, atoms - kb * kAtoms);
 #pragma unroll
-                    for (int at = 0; at < kAtoms; ++at) {
-                        if (at >= here) break;
+                    for (int j = 0; j < kSub; ++j) {
+                        const int acc = acc_of(j);
+                        if (kb == 0 && uses > 0)
+                            ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&bar.acc_empty[acc], (uint32_t)(uses - 1) & 1u, a.status));
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll
-                        for (int kk = 0; kk < kKB / 32; ++kk)  // descriptors count 16-byte units
-                            tc_mma_i8_pair(one, tmem_base + (uint32_t)(acc * kMaxRows), ad + (at * kATile + kk * 32) / 16,
-                                           bd + (at * half * kKB + kk * 32) / 16, idesc, (kb | at | kk) != 0 ? 1u : 0u);
+                        for (int at = 0; at < kAtoms; ++at) {
+                            if (at >= here) break;
+#pragma unroll
+                            for (int kk = 0; kk < kKB / 32; ++kk)  // descriptors count 16-byte units
+                                tc_mma_i8_pair(one, tmem_base + (uint32_t)(acc * kMaxRows),
+                                               ad + (at * kATile + j * 128 * kKB + kk * 32) / 16,
+                                               bd + (at * half * kKB + kk * 32) / 16, idesc, (kb | at | kk) != 0 ? 1u : 0u);
+                        }
+                        if (kb == nkb - 1 && one) tc_commit_pair(&bar.acc_full[acc], 3);
                     }
-                    if (one) tc_commit_pair(&bar.empty[s], 3);
+                    if (ok && one) tc_commit_pair(&bar.empty[s], 3);
                 }
                 if (!ok) {
                     atomicExch(&bar.abort_flag, 1);
                     break;
                 }
-                if (one) tc_commit_pair(&bar.acc_full[acc], 3);
             }
             if (one) tc_commit_pair(&bar.drain, 1);  // completes once every MMA issued above has
             mbar_wait(&bar.drain, 0u, a.status);
@@ -284,21 +311,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else {
         // ---------------- epilogue warps (both CTAs) ----------------
         const int q = warp & 3;            // tensor memory lanes this warp may read
-        const int ch = rank * 128 + q * 32 + lane;
         const int et = threadIdx.x - 64;
+        const int part = ((warp - 2) >> 2) & 1;                  // which half of the 64-column groups
+        const int j = kSub == 1 ? 0 : (warp - 2) / kEpiWarps;    // which 128 of the CTA's channels
         if (!a.offsets) pdl_wait_prior();
-        const int part = (warp - 2) >> 2;  // which half of the 64-column groups
         int ti = 0;
         for (int t = worker; t < total; t += workers, ++ti) {
             const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
-            const int acc = ti & 1;
-            float* rs = row_scale + acc * kMaxRows;
-            for (int i = et; i < w.n; i += 32 * kEpiWarps) rs[i] = a.xs[w.row0 + i];
-            const int c = w.ct * kCh + ch;
+            const int acc = kSub == 1 ? ti & 1 : j, uses = kSub == 1 ? ti >> 1 : ti;
+            float* rs = row_scale + (ti & 1) * kMaxRows;
+            for (int i = et; i < w.n; i += S::kEpi) rs[i] = a.xs[w.row0 + i];
+            const int c = w.ct * kCh + rank * S::kCtaCh + j * 128 + q * 32 + lane;
             const bool cv = c < a.N;
             const float sw = cv ? __half2float(__ushort_as_half(a.ws[(int64_t)w.e * a.N + c])) : 0.0f;
-            if (!named_sync_and(1, 32 * kEpiWarps, !*abort_flag)) break;
-            const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bar.acc_full[acc], (uint32_t)(ti >> 1) & 1u, a.status));
+            if (!named_sync_and(1, S::kEpi, !*abort_flag)) break;
+            const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bar.acc_full[acc], (uint32_t)uses & 1u, a.status));
             tc_fence_after();
             if (!ok) {
                 atomicExch(&bar.abort_flag, 1);
@@ -309,8 +336,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(dcol + (uint32_t)c0, v);
                 tc_wait_ld();
-                if (!cv) continue;
-                w8a8_store_cols(a.Y, a.y_fp32, (int64_t)(w.row0 + c0) * a.N + c, a.N, sw, rs + c0, v, w.n - c0);
+                if (cv)
+                    w8a8_store_cols(a.Y, a.y_fp32, (int64_t)(w.row0 + c0) * a.N + c, a.N, sw, rs + c0, v, w.n - c0);
             }
             tc_fence_before();
             __syncwarp();
@@ -333,54 +360,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-}  // namespace
+int max_of(int a, int b) { return a > b ? a : b; }
 
-cudaError_t launch_w8a8_pair(const W8A8Args& a, int num_sms, bool pdl, cudaStream_t stream) {
+template <int kSub>
+cudaError_t launch_shape(const W8A8Args& a, int step, int pairs, bool pdl, cudaStream_t stream) {
+    using S = Shape<kSub>;
     PairPlan p = {};
-    p.n_ct = ceil_div(a.N, kCh);
-    const int pairs = num_sms / 2;
-    p.step = kMaxRows;
-    if (!a.offsets) {
-        // rows per tile: the fewest waves' worth of L2 reads (128 bytes per
-        // channel and k block, 64 per row)
-        int64_t best = -1;
-        for (int step = kMaxRows; step >= 32; step -= 32) {
-            const int64_t tiles = (int64_t)ceil_div(a.R, step) * p.n_ct;
-            const int64_t cost = (tiles + pairs - 1) / pairs * (128 * 128 + 64 * step);
-            if (best < 0 || cost < best) {
-                best = cost;
-                p.step = step;
-            }
-        }
-    }
-    const int64_t token_tiles = a.offsets ? (int64_t)(a.E < a.R ? a.E : a.R) + a.R / p.step : ceil_div(a.R, p.step);
+    p.step = step;
+    p.n_ct = ceil_div(a.N, S::kCh);
+    const int64_t token_tiles = a.offsets ? (int64_t)(a.E < a.R ? a.E : a.R) + a.R / step : ceil_div(a.R, step);
     const int64_t tiles = token_tiles * p.n_ct;
     if (tiles > 0x3fffffff) return cudaErrorNotSupported;  // tile numbers stay far from overflow
 
     RowMaps tx = {};
     CUtensorMap tw;
-    CUresult cr = encode_tensor_map_k_atoms(&tw, a.qweight, (uint64_t)a.K, (uint64_t)a.E * (uint64_t)a.N, 128, kAtoms);
+    CUresult cr = encode_tensor_map_k_atoms(&tw, a.qweight, (uint64_t)a.K, (uint64_t)a.E * (uint64_t)a.N, S::kCtaCh, S::kAtoms);
     // one matrix: no tile has more rows than the first
-    const int most = ceil_div(ceil_div(a.R, ceil_div(a.R, p.step)), 32) * 16;
-    for (int half = 16; half <= p.step / 2 && cr == CUDA_SUCCESS; half += 16)
+    const int most = ceil_div(ceil_div(a.R, ceil_div(a.R, step)), 32) * 16;
+    for (int half = 16; half <= step / 2 && cr == CUDA_SUCCESS; half += 16)
         if (a.offsets || half <= most)
-            cr = encode_tensor_map_k_atoms(&tx.m[half / 16 - 1], a.Xq, (uint64_t)a.K, (uint64_t)a.R, half, kAtoms);
+            cr = encode_tensor_map_k_atoms(&tx.m[half / 16 - 1], a.Xq, (uint64_t)a.K, (uint64_t)a.R, half, S::kAtoms);
     if (cr != CUDA_SUCCESS) return cudaErrorInvalidValue;
-    const int smem = pair_smem(a.E);
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(w8a8_pair_kernel), 227 * 1024, allowed);
+    const auto kernel = w8a8_pair_kernel<kSub>;
+    cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kernel), 227 * 1024, allowed);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = (size_t)pair_smem<kSub>(a.E);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, w8a8_pair_kernel, tx, tw, a, p);
+    return cudaLaunchKernelEx(&cfg, kernel, tx, tw, a, p);
+}
+
+}  // namespace
+
+cudaError_t launch_w8a8_pair(const W8A8Args& a, int num_sms, bool pdl, cudaStream_t stream) {
+    // Channels and rows per tile, by the time of all waves.  A k atom of a tile
+    // takes as long as its reads from L2 (per CTA 128 bytes per channel, 64 per
+    // row) or as its MMAs, 124 of those bytes per row and 256 channels of the
+    // tile, whichever is longer.  Wide tiles read less but leave the tensor pipe
+    // idle between tiles, and a coarser last wave: for one deep matrix only.
+    // (us, narrow / wide: 8192 x 1024 x 8192 50.7 / 45.1, 4096 x 4096 x 11008
+    // 122 / 117, 8192 x 28672 x 8192 1220 / 1200; but 4096 x 11008 x 4096 118 /
+    // 121, and 8 experts of 4096 x 11008 with 2048 rows each 474 / 502.)
+    const int pairs = num_sms / 2;
+    int sub = 1, step = kMaxRows;
+    int64_t best = -1;
+    for (int u = 1; u <= 2 && !a.offsets; ++u)
+        for (int rows = kMaxRows; rows >= 32 && (u == 1 || a.K >= 8192); rows -= 32) {
+            const int64_t tiles = (int64_t)ceil_div(a.R, rows) * ceil_div(a.N, 256 * u);
+            const int64_t atom = max_of(128 * 128 * u + 64 * rows, 124 * rows * u);
+            const int64_t cost = (tiles + pairs - 1) / pairs * atom;
+            if (best < 0 || cost < best) {
+                best = cost;
+                sub = u;
+                step = rows;
+            }
+        }
+    return sub == 1 ? launch_shape<1>(a, step, pairs, pdl, stream) : launch_shape<2>(a, step, pairs, pdl, stream);
 }
 
 }  // namespace wq
