@@ -229,6 +229,48 @@ def test_tokens_bad_row_index_is_flagged_and_coded_zero():
     assert np.array_equal(got.codes.cpu().numpy(), q) and np.array_equal(got.scales.cpu().numpy(), s)
 
 
+@pytest.mark.parametrize("T,R,K", [(128, 256, 64), (130, 1001, 1056), (200, 4097, 4096), (300, 601, 4128),
+                                   (128, 1500, 8192), (150, 900, 11008), (140, 280, 16384), (130, 300, 16416),
+                                   (1024, 8192, 512)])
+def test_tokens_gathered_into_several_rows(T, R, K):
+    g = torch.Generator().manual_seed(T + R)
+    X = activations(T, K, R)
+    X[3] = 0
+    X[5, 7] = float("nan")
+    X[6, K - 1] = -float("inf")
+    X[7] = X[7] * 2.0 ** -115
+    rows = torch.randint(0, T, (R,), generator=g).to(torch.int32)
+    rows[:9] = torch.tensor([3, 5, 6, 7, 0, T - 1, T - 1, 0, 5])
+    smooth = (torch.rand(K, generator=g) * 4 + 0.1).to(torch.bfloat16)
+    check_tokens(X, rows=rows)
+    check_tokens(X, rows=rows, smooth=smooth)
+    check_tokens(X, rows=torch.full((R,), 5, dtype=torch.int32))   # all rows one token
+    # an index that starts off a 16-byte border
+    b = _b()
+    q, s, _ = ref.quantize_tokens(X[rows[1:].long()])
+    if R - 1 >= 2 * T:
+        got = b.quantize_tokens(X.cuda(), rows.cuda()[1:])
+        assert np.array_equal(got.codes.cpu().numpy(), q) and np.array_equal(got.scales.cpu().numpy(), s)
+        b.device_error()
+
+
+def test_tokens_gathered_into_several_rows_with_bad_indices():
+    b = _b()
+    T, R, K = 160, 2000, 544
+    X = activations(T, K, 21)
+    rows = torch.randint(0, T, (R,), generator=torch.Generator().manual_seed(9)).to(torch.int32)
+    rows[::13] = T
+    rows[1::29] = -(1 << 31)
+    rows[2::31] = (1 << 31) - 1
+    got = b.quantize_tokens(X.cuda(), rows.cuda())
+    st, flags = b.device_error()
+    assert st == b.WQ_ERR_INVALID_ARG and flags == b.WQ_DEVFLAG_INDEX
+    q, s, _ = ref.quantize_tokens(X[rows.clamp(0, T - 1).long()])
+    dead = ((rows < 0) | (rows >= T)).numpy()
+    q[dead], s[dead] = 0, 1
+    assert np.array_equal(got.codes.cpu().numpy(), q) and np.array_equal(got.scales.cpu().numpy(), s)
+
+
 def test_tokens_none_to_gather_from():
     b = _b()
     rows = torch.zeros(3, dtype=torch.int32, device="cuda")
