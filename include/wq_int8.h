@@ -89,6 +89,7 @@ wq_status wq_quantize_tokens(const void* X_bf16, int64_t T, int64_t d_in, const 
  *   d_out        1 .. 2^31 - 1.
  *   d_in         a multiple of 32, 32 .. WQ_INT8_MAX_D_IN.
  *   Y            [M][d_out] output, y_dtype as wq_linear_w4a16.  16-byte aligned.
+ *                May not overlap the inputs.
  * A call may read qweight and scales_fp16 before the kernel ahead of it on the
  * stream has ended, if that kernel allows its successor to start early
  * (programmatic dependent launch: this library's linear layers and

@@ -398,6 +398,7 @@ def test_linear_no_tokens():
     _, _, wq, ws = operands(1, 40, 64, 0)
     x = b.quantize_tokens(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"))
     assert b.linear_w8a8(x, dense(wq, ws)).shape == (0, 40)
+    assert b.linear_w8a8(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), dense(wq, ws)).shape == (0, 40)
     off = torch.zeros(2, dtype=torch.int32, device="cuda")
     assert b.linear_w8a8_grouped(x, experts(wq[None], ws[None]), off).shape == (0, 40)
 
