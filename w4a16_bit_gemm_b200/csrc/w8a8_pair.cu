@@ -407,8 +407,11 @@ cudaError_t launch_w8a8_pair(const W8A8Args& a, int num_sms, bool pdl, cudaStrea
     // tile, whichever is longer.  Wide tiles read less but leave the tensor pipe
     // idle between tiles, and a coarser last wave: for one deep matrix only.
     // (us, narrow / wide: 8192 x 1024 x 8192 50.7 / 45.1, 4096 x 4096 x 11008
-    // 122 / 117, 8192 x 28672 x 8192 1220 / 1200; but 4096 x 11008 x 4096 118 /
-    // 121, and 8 experts of 4096 x 11008 with 2048 rows each 474 / 502.)
+    // 122 / 117, 8192 x 28672 x 8192 back to back 1416 / 1328; but 4096 x 11008 x
+    // 4096 118 / 121, and 8 experts of 4096 x 11008 with 2048 rows each 543 / 555.)
+    // Fewer rows than the most have to win by 3 %: they read more for the same
+    // MMAs, which the power limit charges (8192 x 28672 x 8192 in wide tiles of
+    // 224 / 256 rows: 1180 / 1203 from rest, 1360 / 1325 back to back).
     const int pairs = num_sms / 2;
     int sub = 1, step = kMaxRows;
     int64_t best = -1;
@@ -417,7 +420,7 @@ cudaError_t launch_w8a8_pair(const W8A8Args& a, int num_sms, bool pdl, cudaStrea
             const int64_t tiles = (int64_t)ceil_div(a.R, rows) * ceil_div(a.N, 256 * u);
             const int64_t atom = max_of(128 * 128 * u + 64 * rows, 124 * rows * u);
             const int64_t cost = (tiles + pairs - 1) / pairs * atom;
-            if (best < 0 || cost < best) {
+            if (best < 0 || cost * 100 < best * (rows == kMaxRows ? 100 : 97)) {
                 best = cost;
                 sub = u;
                 step = rows;
