@@ -441,6 +441,15 @@ def test_grouped_skewed_prompt():
     check_grouped(rng.multinomial(1500, rng.dirichlet(np.full(24, 0.4))).tolist(), 640, 512, 7)
 
 
+# up to 128 rows per expert on average, in more than one wave of tiles: experts
+# below, at and above a tile's 160 rows, depths on both sides of the ring's length
+@pytest.mark.parametrize("K", [32, 1024, 1056, 2304])
+@pytest.mark.parametrize("counts", [[70] * 40, [0, 161, 159, 160, 1, 321, 96, 0, 0, 200] * 5, [5000] + [0] * 39,
+                                    [3] * 39 + [2900]])
+def test_grouped_medium_loads(counts, K):
+    check_grouped(counts, 648, K, len(counts) + K, torch.float32 if K % 128 else torch.bfloat16, before=3, behind=5)
+
+
 def test_grouped_leaves_other_rows_as_they_were():
     check_grouped([3, 0, 20], 130, 160, 1, before=7, behind=9)
     check_grouped([300, 280], 130, 160, 2, torch.float32, before=1, behind=300)
