@@ -81,9 +81,10 @@ struct TokenArgs {
 };
 
 // LANES threads per row (32 ... 1024), NV 16-byte pieces of the row per thread
-// in registers; NV = 0: rows too long for that are read twice.
-template <int LANES, int NV>
-__global__ void __launch_bounds__(block_threads(LANES)) quantize_tokens_kernel(const TokenArgs a) {
+// in registers; NV = 0: rows too long for that are read twice.  At least
+// BLOCKS blocks fit an SM.
+template <int LANES, int NV, int BLOCKS>
+__global__ void __launch_bounds__(block_threads(LANES), BLOCKS) quantize_tokens_kernel(const TokenArgs a) {
     constexpr int kThreads = block_threads(LANES), kRows = kThreads / LANES, kWarps = LANES / 32;
     __shared__ float part[kThreads / 32], part2[kThreads / 32], part3[kThreads / 32];
     const int l = threadIdx.x % LANES, sub = threadIdx.x / LANES;
@@ -177,11 +178,17 @@ __global__ void __launch_bounds__(block_threads(LANES)) quantize_tokens_kernel(c
     }
 }
 
+// As many registers as let all blocks of 256 threads run at once, 4 to 6 to an
+// SM (52, 47 and 40 registers a thread).  us, 4 / 5 / 6 blocks: 300 x 8192
+// smoothed 4.8 / 5.3 / 5.1, 1200 x 4096 smoothed 6.8 / 6.1 / 6.7, 8192 x 8192
+// - / 34.4 / 32.3, smoothed - / 44.0 / 42.4; 7 and 8 blocks (36 and 32
+// registers) are no faster.
 template <int LANES, int NV>
-cudaError_t launch_tokens(const TokenArgs& a, bool pdl, cudaStream_t stream) {
+cudaError_t launch_tokens(const TokenArgs& a, int num_sms, bool pdl, cudaStream_t stream) {
     constexpr int kRows = block_threads(LANES) / LANES;
+    const int64_t blocks = ((int64_t)a.R + kRows - 1) / kRows;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((int64_t)a.R + kRows - 1) / kRows));
+    cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(block_threads(LANES));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -189,14 +196,20 @@ cudaError_t launch_tokens(const TokenArgs& a, bool pdl, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, quantize_tokens_kernel<LANES, NV>, a);
+    if constexpr (NV == 4) {
+        if (blocks > 5 * num_sms) return cudaLaunchKernelEx(&cfg, quantize_tokens_kernel<LANES, NV, 6>, a);
+        if (blocks > 4 * num_sms) return cudaLaunchKernelEx(&cfg, quantize_tokens_kernel<LANES, NV, 5>, a);
+        return cudaLaunchKernelEx(&cfg, quantize_tokens_kernel<LANES, NV, 4>, a);
+    } else {
+        return cudaLaunchKernelEx(&cfg, quantize_tokens_kernel<LANES, NV, 1024 / LANES>, a);
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_quantize_tokens(const void* X, int64_t T, int64_t K, const int32_t* rows, int64_t R,
-                                   const void* smooth, int8_t* Xq, float* x_scales, uint32_t* status, bool pdl,
-                                   cudaStream_t stream) {
+                                   const void* smooth, int8_t* Xq, float* x_scales, uint32_t* status, int num_sms,
+                                   bool pdl, cudaStream_t stream) {
     TokenArgs a = {};
     a.X = static_cast<const uint16_t*>(X);
     a.rows = rows;
@@ -210,14 +223,14 @@ cudaError_t launch_quantize_tokens(const void* X, int64_t T, int64_t K, const in
     // 4 pieces (64 bytes) per thread hide the load latency; longer rows take
     // more registers before they take a second pass
     const int64_t pieces = K / 8;
-    if (pieces <= 32 * 4) return launch_tokens<32, 4>(a, pdl, stream);
-    if (pieces <= 64 * 4) return launch_tokens<64, 4>(a, pdl, stream);
-    if (pieces <= 128 * 4) return launch_tokens<128, 4>(a, pdl, stream);
-    if (pieces <= 256 * 4) return launch_tokens<256, 4>(a, pdl, stream);
-    if (pieces <= 256 * 8) return launch_tokens<256, 8>(a, pdl, stream);
-    if (pieces <= 512 * 8) return launch_tokens<512, 8>(a, pdl, stream);
-    if (pieces <= 1024 * 8) return launch_tokens<1024, 8>(a, pdl, stream);
-    return launch_tokens<1024, 0>(a, pdl, stream);
+    if (pieces <= 32 * 4) return launch_tokens<32, 4>(a, num_sms, pdl, stream);
+    if (pieces <= 64 * 4) return launch_tokens<64, 4>(a, num_sms, pdl, stream);
+    if (pieces <= 128 * 4) return launch_tokens<128, 4>(a, num_sms, pdl, stream);
+    if (pieces <= 256 * 4) return launch_tokens<256, 4>(a, num_sms, pdl, stream);
+    if (pieces <= 256 * 8) return launch_tokens<256, 8>(a, num_sms, pdl, stream);
+    if (pieces <= 512 * 8) return launch_tokens<512, 8>(a, num_sms, pdl, stream);
+    if (pieces <= 1024 * 8) return launch_tokens<1024, 8>(a, num_sms, pdl, stream);
+    return launch_tokens<1024, 0>(a, num_sms, pdl, stream);
 }
 
 }  // namespace wq
