@@ -167,6 +167,32 @@ def test_tokens_smoothed_many_rows(R, K):
     check_tokens(X, smooth=smooth)
 
 
+# 148 SMs: both sides of the row counts where a block gets fewer registers or a row fewer threads
+@pytest.mark.parametrize("R,K", [(592, 8192), (593, 8192), (740, 8192), (741, 8192), (1185, 4096), (1481, 2080),
+                                 (148, 20000), (149, 20000), (296, 11008), (297, 11008)])
+def test_tokens_row_counts(R, K):
+    X = activations(R, K, R)
+    X[R - 1, K - 1] = float("inf")
+    X[R // 2] = 0
+    smooth = (torch.rand(K, generator=torch.Generator().manual_seed(K)) * 4 + 0.1).to(torch.bfloat16)
+    check_tokens(X)
+    check_tokens(X, smooth=smooth)
+    smooth[K - 1], smooth[K // 2] = 0.0, 3e38
+    check_tokens(X, smooth=smooth)
+
+
+@pytest.mark.parametrize("R,K", [(1, 4096), (3, 11008), (3, 20000), (700, 8192), (2000, 1056)])
+def test_tokens_smoothing_scales_off_16_bytes(R, K):
+    b = _b()
+    X = activations(R, K, 31)
+    held = (torch.rand(K + 8, generator=torch.Generator().manual_seed(5)) * 4 + 0.1).to(torch.bfloat16)
+    for shift in (1, 4):
+        smooth = held[shift:shift + K]
+        q, s, _ = ref.quantize_tokens(ref.smoothed(X, smooth))
+        got = b.quantize_tokens(X.cuda(), smooth=held.cuda()[shift:shift + K])
+        assert np.array_equal(got.codes.cpu().numpy(), q) and np.array_equal(got.scales.cpu().numpy(), s)
+
+
 def test_tokens_smoothed_many_rows_with_bad_indices():
     b = _b()
     R, K = 3000, 4096
