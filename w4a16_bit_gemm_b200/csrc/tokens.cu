@@ -5,11 +5,9 @@
 // the row is gathered through an index.  Bound by HBM: 2 bytes in, 1 out per
 // value, so a row is read once and kept in registers between its maximum and
 // its codes.  The arithmetic is in tokens_device.cuh.  Measured: 8192 x 8192
-// 33 us (6.1 TB/s, 93 % of the copy rate), smoothed 42 us; 16384 x 11008 89 us
-// (93 %); one row of 4096 1.6 us, smoothed 1.9.  Issue takes about half of the
-// cycles (10 instructions per value).  Smoothed, two rows per thread with one
-// set of reciprocals are no faster (8192 x 8192 45 us): what is missing is
-// bytes in flight while the longer arithmetic runs.
+// 34 us (5.9 TB/s, 90 % of the copy rate), smoothed 44 us; 16384 x 11008 89 us
+// (93 %); one row of 4096 1.7 us.  Issue takes about half of the cycles (10
+// instructions per value).
 #include <stdint.h>
 
 #include "tokens_device.cuh"
@@ -83,10 +81,9 @@ struct TokenArgs {
 };
 
 // LANES threads per row (32 ... 1024), NV 16-byte pieces of the row per thread
-// in registers; NV = 0: rows too long for that are read twice.  At least
-// BLOCKS blocks fit an SM.
-template <int LANES, int NV, int BLOCKS>
-__global__ void __launch_bounds__(block_threads(LANES), BLOCKS) quantize_tokens_kernel(const TokenArgs a) {
+// in registers; NV = 0: rows too long for that are read twice.
+template <int LANES, int NV>
+__global__ void __launch_bounds__(block_threads(LANES)) quantize_tokens_kernel(const TokenArgs a) {
     constexpr int kThreads = block_threads(LANES), kRows = kThreads / LANES, kWarps = LANES / 32;
     __shared__ float part[kThreads / 32], part2[kThreads / 32], part3[kThreads / 32];
     const int l = threadIdx.x % LANES, sub = threadIdx.x / LANES;
@@ -115,10 +112,6 @@ __global__ void __launch_bounds__(block_threads(LANES), BLOCKS) quantize_tokens_
         return exact ? smooth8_exact(v, sm) : smooth8(v, sm, largest);
     };
 
-    // With 64 registers a thread all smoothing scales can be fetched at once: a
-    // wait for each piece's took 0.5 us on the way (1 x 4096 2.45 -> 1.87 us,
-    // 300 x 8192 4.8 -> 4.5).
-    constexpr bool kTogether = NV == 4 && BLOCKS * kThreads == 1024;
     constexpr int kHold = NV > 0 ? NV : 1;
     uint4 held[kHold];
     if constexpr (NV > 0) {
@@ -128,22 +121,10 @@ __global__ void __launch_bounds__(block_threads(LANES), BLOCKS) quantize_tokens_
             held[i] = live && c < pieces ? load_row16(x + 8 * c) : zero;
         }
         if (smoothed) {
-            if (kTogether && (reinterpret_cast<uintptr_t>(a.smooth) & 15) == 0) {
-                uint4 sm[NV];
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int c = l + i * LANES;
-                    if (c < pieces) sm[i] = load_smooth16(a.smooth + 8 * c);
-                }
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (l + i * LANES < pieces) held[i] = smooth8(held[i], sm[i], largest);
-            } else {
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int c = l + i * LANES;
-                    if (c < pieces) held[i] = smooth8(held[i], load_smooth(a.smooth, 8 * c), largest);
-                }
+            for (int i = 0; i < NV; ++i) {
+                const int c = l + i * LANES;
+                if (c < pieces) held[i] = smooth8(held[i], load_smooth(a.smooth, 8 * c), largest);
             }
         }
 #pragma unroll
@@ -196,17 +177,11 @@ __global__ void __launch_bounds__(block_threads(LANES), BLOCKS) quantize_tokens_
     }
 }
 
-// As many registers as let all blocks of 256 threads run at once, 4 to 6 to an
-// SM (52, 47 and 40 registers a thread).  us, 4 / 5 / 6 blocks: 300 x 8192
-// smoothed 4.8 / 5.3 / 5.1, 1200 x 4096 smoothed 6.8 / 6.1 / 6.7, 8192 x 8192
-// - / 34.4 / 32.3, smoothed - / 44.0 / 42.4; 7 and 8 blocks (36 and 32
-// registers) are no faster.
 template <int LANES, int NV>
-cudaError_t launch_tokens(const TokenArgs& a, int num_sms, bool pdl, cudaStream_t stream) {
+cudaError_t launch_tokens(const TokenArgs& a, bool pdl, cudaStream_t stream) {
     constexpr int kRows = block_threads(LANES) / LANES;
-    const int64_t blocks = ((int64_t)a.R + kRows - 1) / kRows;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.R + kRows - 1) / kRows));
     cfg.blockDim = dim3(block_threads(LANES));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -214,20 +189,14 @@ cudaError_t launch_tokens(const TokenArgs& a, int num_sms, bool pdl, cudaStream_
     attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if constexpr (NV == 4 && LANES <= 256) {
-        if (blocks > 5 * num_sms) return cudaLaunchKernelEx(&cfg, quantize_tokens_kernel<LANES, NV, 6>, a);
-        if (blocks > 4 * num_sms) return cudaLaunchKernelEx(&cfg, quantize_tokens_kernel<LANES, NV, 5>, a);
-        return cudaLaunchKernelEx(&cfg, quantize_tokens_kernel<LANES, NV, 4>, a);
-    } else {
-        return cudaLaunchKernelEx(&cfg, quantize_tokens_kernel<LANES, NV, 1024 / LANES>, a);
-    }
+    return cudaLaunchKernelEx(&cfg, quantize_tokens_kernel<LANES, NV>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_quantize_tokens(const void* X, int64_t T, int64_t K, const int32_t* rows, int64_t R,
-                                   const void* smooth, int8_t* Xq, float* x_scales, uint32_t* status, int num_sms,
-                                   bool pdl, cudaStream_t stream) {
+                                   const void* smooth, int8_t* Xq, float* x_scales, uint32_t* status, bool pdl,
+                                   cudaStream_t stream) {
     TokenArgs a = {};
     a.X = static_cast<const uint16_t*>(X);
     a.rows = rows;
@@ -241,18 +210,14 @@ cudaError_t launch_quantize_tokens(const void* X, int64_t T, int64_t K, const in
     // 4 pieces (64 bytes) per thread hide the load latency; longer rows take
     // more registers before they take a second pass
     const int64_t pieces = K / 8;
-    if (pieces <= 32 * 4) return launch_tokens<32, 4>(a, num_sms, pdl, stream);
-    if (pieces <= 64 * 4) return launch_tokens<64, 4>(a, num_sms, pdl, stream);
-    if (pieces <= 128 * 4) return launch_tokens<128, 4>(a, num_sms, pdl, stream);
-    if (pieces <= 256 * 4) return launch_tokens<256, 4>(a, num_sms, pdl, stream);
-    // (few longer rows: more threads instead; 1 x 11008 2.08 -> 1.97 us, smoothed
-    // 3.65 -> 2.36, 148 x 16384 smoothed 5.7 -> 3.9)
-    if (R <= 2 * num_sms && pieces <= 512 * 4) return launch_tokens<512, 4>(a, num_sms, pdl, stream);
-    if (R <= num_sms && pieces <= 1024 * 4) return launch_tokens<1024, 4>(a, num_sms, pdl, stream);
-    if (pieces <= 256 * 8) return launch_tokens<256, 8>(a, num_sms, pdl, stream);
-    if (pieces <= 512 * 8) return launch_tokens<512, 8>(a, num_sms, pdl, stream);
-    if (pieces <= 1024 * 8) return launch_tokens<1024, 8>(a, num_sms, pdl, stream);
-    return launch_tokens<1024, 0>(a, num_sms, pdl, stream);
+    if (pieces <= 32 * 4) return launch_tokens<32, 4>(a, pdl, stream);
+    if (pieces <= 64 * 4) return launch_tokens<64, 4>(a, pdl, stream);
+    if (pieces <= 128 * 4) return launch_tokens<128, 4>(a, pdl, stream);
+    if (pieces <= 256 * 4) return launch_tokens<256, 4>(a, pdl, stream);
+    if (pieces <= 256 * 8) return launch_tokens<256, 8>(a, pdl, stream);
+    if (pieces <= 512 * 8) return launch_tokens<512, 8>(a, pdl, stream);
+    if (pieces <= 1024 * 8) return launch_tokens<1024, 8>(a, pdl, stream);
+    return launch_tokens<1024, 0>(a, pdl, stream);
 }
 
 }  // namespace wq

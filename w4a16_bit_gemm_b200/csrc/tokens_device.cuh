@@ -1,4 +1,5 @@
-// tokens_device.cuh -- the arithmetic of per-token INT8 codes (sm_100a only).
+// tokens_device.cuh -- the arithmetic of per-token INT8 codes (sm_100a only),
+// shared by the quantizer and by the linear layer that quantizes its own rows.
 //
 //   s = fl32(max |x| / 127) over a row's finite values (1 if 0),
 //   q = clamp(rint(fl32(x / s)), -127, 127); NaN -> 0, +-Inf -> +-127.
@@ -36,16 +37,6 @@ __device__ __forceinline__ void unpack8(const uint4& v, float f[8]) {
 __device__ __forceinline__ uint4 load_row16(const uint16_t* p) {
     uint4 r;
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p)
-                 : "memory");
-    return r;
-}
-
-// 8 smoothing scales, 16-byte aligned; the load stays where it stands.
-__device__ __forceinline__ uint4 load_smooth16(const uint16_t* p) {
-    uint4 r;
-    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                  : "l"(p)
                  : "memory");

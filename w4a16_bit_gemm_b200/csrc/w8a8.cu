@@ -105,7 +105,7 @@ wq_status wq_quantize_tokens(const void* X_bf16, int64_t T, int64_t d_in, const 
     if (v != WQ_OK) return v;
     if (R == 0) return WQ_OK;
     const cudaError_t e = launch_quantize_tokens(X_bf16, T, d_in, rows, R, smooth_bf16, Xq, x_scales, status,
-                                                 num_sms, pdl_enabled(), static_cast<cudaStream_t>(stream));
+                                                 pdl_enabled(), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
 

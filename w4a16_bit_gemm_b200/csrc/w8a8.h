@@ -25,8 +25,8 @@ CUresult encode_tensor_map_k_atoms(CUtensorMap* map, const void* base, uint64_t 
                                    int atoms);
 
 cudaError_t launch_quantize_tokens(const void* X, int64_t T, int64_t K, const int32_t* rows, int64_t R,
-                                   const void* smooth, int8_t* Xq, float* x_scales, uint32_t* status, int num_sms,
-                                   bool pdl, cudaStream_t stream);
+                                   const void* smooth, int8_t* Xq, float* x_scales, uint32_t* status, bool pdl,
+                                   cudaStream_t stream);
 
 // One product: R rows against one weight matrix (offsets == nullptr, E == 1)
 // or against the matrix of the expert that holds each row.

@@ -33,21 +33,20 @@ namespace wq {
 namespace {
 
 constexpr int kKB = 128;                 // k per swizzle atom
-constexpr int kMaxRows = 256;            // rows per tile, columns of an accumulator
+constexpr int kMaxRows = 256;            // rows per tile
+constexpr int kBTile = 128 * kKB;        // bytes of rows per CTA and atom
 constexpr int kEpiWarps = 8;             // per accumulator of a tile
 constexpr int kTmemCols = 2 * kMaxRows;
 
 // kSub = 1: tiles of 256 channels, 128 per CTA; the two accumulators belong to
 // successive tiles.  kSub = 2: tiles of 512 channels, 256 per CTA; each
 // accumulator takes 128 of them, and a row is fetched once for both.
-// kRows: most rows of a tile; the room that 160 leave holds a fourth stage.
-template <int kSub, int kRows>
+template <int kSub>
 struct Shape {
     static constexpr int kCh = 256 * kSub;           // channels per tile
     static constexpr int kCtaCh = 128 * kSub;        // channels per CTA
     static constexpr int kAtoms = kSub == 1 ? 2 : 1; // atoms per stage
-    static constexpr int kStages = kSub == 1 && kRows > 160 ? 3 : 4;
-    static constexpr int kBTile = kRows / 2 * kKB;   // bytes of rows per CTA and atom
+    static constexpr int kStages = kSub == 1 ? 3 : 4;
     static constexpr int kATile = kCtaCh * kKB;      // bytes of weights per CTA and atom
     static constexpr int kEpi = 32 * kEpiWarps * kSub;  // epilogue threads
     static constexpr int kThreads = 64 + kEpi;       // copy warp, MMA warp, epilogue warps
@@ -76,14 +75,13 @@ struct PairBars {
 };
 
 __host__ __device__ constexpr int table_ints(int E) { return (E + 1 + 3) & ~3; }
-template <int kSub, int kRows>
+template <int kSub>
 __host__ __device__ constexpr int pair_smem(int E) {
-    using S = Shape<kSub, kRows>;
-    return 1024 + S::kStages * S::kAtoms * (S::kATile + S::kBTile) + 2 * kMaxRows * 4 + 2 * table_ints(E) * 4 + 64 * 4 +
+    using S = Shape<kSub>;
+    return 1024 + S::kStages * S::kAtoms * (S::kATile + kBTile) + 2 * kMaxRows * 4 + 2 * table_ints(E) * 4 + 64 * 4 +
            (int)sizeof(PairBars);
 }
-static_assert(pair_smem<1, 256>(WQ_INT8_MAX_EXPERTS) <= 227 * 1024 && pair_smem<1, 160>(WQ_INT8_MAX_EXPERTS) <= 227 * 1024 &&
-                  pair_smem<2, 256>(1) <= 227 * 1024,
+static_assert(pair_smem<1>(WQ_INT8_MAX_EXPERTS) <= 227 * 1024 && pair_smem<2>(WQ_INT8_MAX_EXPERTS) <= 227 * 1024,
               "pair kernel shared memory");
 
 __device__ __forceinline__ void tc_mma_i8_pair(bool one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -146,12 +144,12 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     }
 }
 
-template <int kSub, int kRows>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub, kRows>::kThreads, 1)
+template <int kSub>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub>::kThreads, 1)
     w8a8_pair_kernel(const __grid_constant__ RowMaps tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                      const W8A8Args a, const PairPlan p) {
-    using S = Shape<kSub, kRows>;
-    constexpr int kCh = S::kCh, kAtoms = S::kAtoms, kStages = S::kStages, kATile = S::kATile, kBTile = S::kBTile;
+    using S = Shape<kSub>;
+    constexpr int kCh = S::kCh, kAtoms = S::kAtoms, kStages = S::kStages, kATile = S::kATile;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* smem_a = smem;
@@ -364,9 +362,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub, kRows>::
 
 int max_of(int a, int b) { return a > b ? a : b; }
 
-template <int kSub, int kRows>
+template <int kSub>
 cudaError_t launch_shape(const W8A8Args& a, int step, int pairs, bool pdl, cudaStream_t stream) {
-    using S = Shape<kSub, kRows>;
+    using S = Shape<kSub>;
     PairPlan p = {};
     p.step = step;
     p.n_ct = ceil_div(a.N, S::kCh);
@@ -384,13 +382,13 @@ cudaError_t launch_shape(const W8A8Args& a, int step, int pairs, bool pdl, cudaS
             cr = encode_tensor_map_k_atoms(&tx.m[half / 16 - 1], a.Xq, (uint64_t)a.K, (uint64_t)a.R, half, S::kAtoms);
     if (cr != CUDA_SUCCESS) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> allowed{0};
-    const auto kernel = w8a8_pair_kernel<kSub, kRows>;
+    const auto kernel = w8a8_pair_kernel<kSub>;
     cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kernel), 227 * 1024, allowed);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
     cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = (size_t)pair_smem<kSub, kRows>(a.E);
+    cfg.dynamicSmemBytes = (size_t)pair_smem<kSub>(a.E);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -428,15 +426,7 @@ cudaError_t launch_w8a8_pair(const W8A8Args& a, int num_sms, bool pdl, cudaStrea
                 step = rows;
             }
         }
-    // Experts with 128 rows or fewer on average, in more than one wave, are bound
-    // by the weights' way from HBM: a fourth stage in flight for tiles of at most
-    // 160 rows.  (us, 256 rows and 3 stages / 160 and 4: 64 experts of 2048 x 4096,
-    // 70 rows each 93.3 / 89.8, 128 rows 97.9 / 94.6; 8 of 4096 x 11008, 70 rows
-    // 65.3 / 62.3; but 200 rows 74.1 / 87.3, and in one wave 8 of 2048 x 4096, 125
-    // rows unevenly 26.9 / 30.3.)
-    if (a.offsets && a.R <= 128 * (int64_t)a.E && (int64_t)a.E * ceil_div(a.N, 256) > pairs)
-        return launch_shape<1, 160>(a, 160, pairs, pdl, stream);
-    return sub == 2 ? launch_shape<2, 256>(a, step, pairs, pdl, stream) : launch_shape<1, 256>(a, step, pairs, pdl, stream);
+    return sub == 1 ? launch_shape<1>(a, step, pairs, pdl, stream) : launch_shape<2>(a, step, pairs, pdl, stream);
 }
 
 }  // namespace wq
