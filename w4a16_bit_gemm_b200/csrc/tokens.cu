@@ -5,8 +5,8 @@
 // the row is gathered through an index.  Bound by HBM: 2 bytes in, 1 out per
 // value, so a row is read once and kept in registers between its maximum and
 // its codes.  The arithmetic is in tokens_device.cuh.  Measured: 8192 x 8192
-// 34 us (5.9 TB/s, 90 % of the copy rate), smoothed 44 us; 16384 x 11008 89 us
-// (93 %); one row of 4096 1.7 us.  Issue takes about half of the cycles (10
+// 34.4 us (5.9 TB/s, 89 % of the copy rate), smoothed 44 us; 16384 x 11008 89 us
+// (93 %); one row of 4096 1.6 us.  Issue takes about half of the cycles (10
 // instructions per value).
 #include <stdint.h>
 

@@ -1,5 +1,4 @@
-// tokens_device.cuh -- the arithmetic of per-token INT8 codes (sm_100a only),
-// shared by the quantizer and by the linear layer that quantizes its own rows.
+// tokens_device.cuh -- the arithmetic of per-token INT8 codes (sm_100a only).
 //
 //   s = fl32(max |x| / 127) over a row's finite values (1 if 0),
 //   q = clamp(rint(fl32(x / s)), -127, 127); NaN -> 0, +-Inf -> +-127.

@@ -16,13 +16,14 @@
 // the tiles in steps of the number of pairs.  Every wait is bounded
 // (WQ_DEVFLAG_TIMEOUT).
 //
-// Bound by the tensor pipe (87 % of active cycles) and, in long runs, by the
-// power cap: 2048 x 8192 x 8192 89 us (3074 TOPS, 93 % of twice the bf16 rate
-// of cuBLAS), 8192 x 28672 x 8192 1.22 to 1.27 ms in a burst.  On the way: 1-SM
-// tiles 153 us and 1.82 ms; pairs 103 us and 1.37 ms; two atoms per stage and
-// copy, so that the issuing threads keep up, and an epilogue of eight warps
-// without a test per column 89 us.  Small products add about 7 us of start,
-// last epilogue and hand-off (512 x 8192 x 8192 28.3 us).
+// Bound by the tensor pipe (84 to 88 % of active cycles) and, in long runs, by
+// the power cap: 2048 x 8192 x 8192 89 us (3080 TOPS, 93 % of twice the bf16
+// rate of cuBLAS), 8192 x 28672 x 8192 1.20 to 1.23 ms in a burst, 1.33 to 1.35
+// ms back to back, 8192 x 1024 x 8192 46 us.  On the way: 1-SM tiles 153 us and
+// 1.82 ms; pairs 103 us and 1.37 ms; two atoms per stage and copy, so that the
+// issuing threads keep up, and an epilogue of eight warps without a test per
+// column 89 us and 1.24 ms (1.45 back to back); tiles of 512 channels.  Small products add about 7 us of start,
+// last epilogue and hand-off (512 x 8192 x 8192 28.5 us).
 #include <stdint.h>
 
 #include "w8a8.h"
