@@ -476,6 +476,33 @@ def test_grouped_medium_loads(counts, K):
     check_grouped(counts, 648, K, len(counts) + K, torch.float32 if K % 128 else torch.bfloat16, before=3, behind=5)
 
 
+def test_grouped_from_bf16_chain_at_full_size():
+    """Quantizer and loaded experts in a row, many times without a wait between."""
+    b = _b()
+    E, N, K, R, T = 64, 2048, 4096, 8192, 1024
+    g = torch.Generator(device="cuda").manual_seed(11)
+    counts = (torch.rand(E, generator=g, device="cuda") ** 2 * 255).long()
+    counts[-1] += R - counts.sum()
+    assert counts.min() >= 0
+    off = torch.nn.functional.pad(counts.cumsum(0), (1, 0)).to(torch.int32)
+    rows = (torch.randperm(R, generator=g, device="cuda") % T).to(torch.int32)
+    X = torch.randn(T, K, generator=g, device="cuda").to(torch.bfloat16)
+    codes = torch.randint(-127, 128, (E, N, K), generator=g, device="cuda", dtype=torch.int8)
+    p = b.PackedExpertsW8(codes.view(torch.int32), torch.rand(E, N, generator=g, device="cuda").half())
+    y = b.linear_w8a8_grouped(X, p, off, rows=rows)
+    torch.cuda.synchronize()
+    outs = [torch.empty_like(y) for _ in range(3)]
+    for i in range(400):
+        b.linear_w8a8_grouped(X, p, off, rows=rows, out=outs[i % 3])
+    torch.cuda.synchronize()
+    assert b.device_error() == (b.WQ_OK, 0)
+    assert all(torch.equal(o, y) for o in outs)
+    e = int(counts.argmax())
+    lo = int(off[e])
+    want = b.linear_w8a8(X[rows[lo:lo + 70].long()], b.PackedLinearW8(p.qweight[e], p.scales[e], N, K, K))
+    assert torch.equal(y[lo:lo + 70], want)
+
+
 def test_grouped_leaves_other_rows_as_they_were():
     check_grouped([3, 0, 20], 130, 160, 1, before=7, behind=9)
     check_grouped([300, 280], 130, 160, 2, torch.float32, before=1, behind=300)
