@@ -22,8 +22,9 @@
 // ms back to back, 8192 x 1024 x 8192 46 us.  On the way: 1-SM tiles 153 us and
 // 1.82 ms; pairs 103 us and 1.37 ms; two atoms per stage and copy, so that the
 // issuing threads keep up, and an epilogue of eight warps without a test per
-// column 89 us and 1.24 ms (1.45 back to back); tiles of 512 channels.  Small products add about 7 us of start,
-// last epilogue and hand-off (512 x 8192 x 8192 28.5 us).
+// column 89 us and 1.24 ms (1.45 back to back); tiles of 512 channels.  Small
+// products add about 7 us of start, last epilogue and hand-off (512 x 8192 x
+// 8192 28.5 us).
 #include <stdint.h>
 
 #include "w8a8.h"
