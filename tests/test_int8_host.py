@@ -140,3 +140,30 @@ def test_reference_words_are_the_w8_layout():
     W = torch.randn(5, 64, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
     oq, _, _, codes = oracle.quantize_pack8(W.view(torch.int16).numpy().view(np.uint16), 64)
     assert np.array_equal(ref.words(codes.astype(np.int8)).numpy().view(np.uint32), oq)
+
+
+# Orders inside the kernels that no run can be asked to show: what goes wrong
+# without them may not end.
+
+def kernel_source(name, start):
+    """The body of the kernel that `start` opens, without comments, in one line."""
+    src = open(os.path.join(ROOT, "w4a16_bit_gemm_b200", "csrc", name)).read()
+    src = re.sub(r"//[^\n]*", "", src)
+    body = src[src.index(start):]
+    return " ".join(body[:body.index("\n}\n")].split())
+
+
+def in_order(body, *parts):
+    at = [0]
+    for p in parts:
+        assert p in body[at[-1]:], (p, "missing, or before", parts)
+        at.append(body.index(p, at[-1]) + len(p))
+
+
+def test_pair_kernel_allocates_once_both_ctas_run():
+    """The allocation of a CTA pair waits without a limit for a warp of each: a
+    barrier of the cluster comes first, and another before the first use and
+    before the memory is given back."""
+    body = kernel_source("w8a8_pair.cu", "w8a8_pair_kernel(")
+    barrier = "cluster_arrive(); cluster_wait();"
+    in_order(body, barrier, "tcgen05.alloc", barrier, "tc_mma_i8_pair", barrier, "tcgen05.dealloc")

@@ -182,7 +182,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub>::kThread
         bar.abort_flag = 0;
         fence_mbar_init();
     }
+    // Both CTAs run before either allocates: the allocation is one operation of
+    // the two, made by a warp of each, and has no limit.  A CTA's blocks start
+    // when its SM gets to them, which other kernels' blocks can put off.
+    cluster_arrive();
+    cluster_wait();
     if (warp == 1) {
+        __syncwarp();
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar.tmem_slot)),
                      "r"((uint32_t)kTmemCols)
                      : "memory");
@@ -196,7 +202,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub>::kThread
     // once this one has ended (launch_shape).
     if (!a.offsets) pdl_launch_dependents();
     cluster_arrive();
-    cluster_wait();  // both CTAs' barriers are initialised
+    cluster_wait();  // both CTAs' barriers are initialised, both have their tensor memory
     tc_fence_after();
     const uint32_t tmem_base = bar.tmem_slot;
     const int total = cum[a.E] * p.n_ct;
@@ -357,6 +363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub>::kThread
     cluster_arrive();
     cluster_wait();
     if (warp == 1) {
+        __syncwarp();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"((uint32_t)kTmemCols)
                      : "memory");
