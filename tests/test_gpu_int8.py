@@ -730,6 +730,26 @@ def test_back_to_back_launches_keep_their_order():
         assert torch.equal(cur, first)
 
 
+@pytest.mark.parametrize("M,N,K", [(70, 512, 512), (300, 2000, 1056), (2100, 1000, 1024), (1100, 600, 8192)])
+def test_many_rows_from_bf16_back_to_back(M, N, K):
+    """Quantizer and SM-pair product in turn, the buffers of one call freed for
+    the next: dense and by expert."""
+    b = _b()
+    _, _, wq, ws = operands(1, N, K, 3, 4)
+    X = activations(M, K, 4)
+    p, pe = dense(wq[1], ws[1]), experts(wq, ws)
+    off = [0, M // 2, M // 2, M - 5, M]
+    xq, xs, _ = ref.quantize_tokens(X)
+    X, offsets = X.cuda(), torch.tensor(off, dtype=torch.int32, device="cuda")
+    held = torch.zeros(M, N)
+    for call, want in ((lambda: b.linear_w8a8(X, p, out_dtype=torch.float32), ref.product(xq, xs, wq[1], ws[1])),
+                       (lambda: b.linear_w8a8_grouped(X, pe, offsets, out_dtype=torch.float32),
+                        ref.grouped(xq, xs, wq, ws, off, held))):
+        outs = [call() for _ in range(12)]
+        ref.check(outs[0], *want)
+        assert all(torch.equal(o, outs[0]) for o in outs[1:])
+
+
 def test_mixed_with_the_other_linear_layers():
     """Kernels that start early beside each other and share tensor memory: 4-bit
     and 8-bit layers of every path in one stream, many times over."""

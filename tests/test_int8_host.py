@@ -167,3 +167,12 @@ def test_pair_kernel_allocates_once_both_ctas_run():
     body = kernel_source("w8a8_pair.cu", "w8a8_pair_kernel(")
     barrier = "cluster_arrive(); cluster_wait();"
     in_order(body, barrier, "tcgen05.alloc", barrier, "tc_mma_i8_pair", barrier, "tcgen05.dealloc")
+
+
+def test_pair_kernel_never_runs_beside_another():
+    """Neither started early nor a starter of others: no wait for an earlier
+    kernel can then hold an SM, or tensor memory, that the pair needs."""
+    src = open(os.path.join(ROOT, "w4a16_bit_gemm_b200", "csrc", "w8a8_pair.cu")).read()
+    src = re.sub(r"//[^\n]*", "", src)
+    for word in ("pdl_launch_dependents", "pdl_wait_prior", "griddepcontrol", "ProgrammaticStreamSerialization"):
+        assert word not in src, word

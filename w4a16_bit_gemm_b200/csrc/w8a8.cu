@@ -76,8 +76,7 @@ cudaError_t run_product(const W8A8Args& a, int num_sms, cudaStream_t stream) {
     const int64_t n_ct = (a.N + 255) / 256;
     const bool few_tiles = a.offsets ? (experts + a.R / 256) * n_ct < pairs / 4 : (a.R + 31) / 32 * n_ct < pairs;
     const bool streams = a.R <= 64 * experts || (few_tiles && a.K >= 2048);
-    const auto launch = streams ? launch_w8a8_stream : launch_w8a8_pair;
-    return launch(a, num_sms, pdl_enabled(), stream);
+    return streams ? launch_w8a8_stream(a, num_sms, pdl_enabled(), stream) : launch_w8a8_pair(a, num_sms, stream);
 }
 
 wq_status product_of_codes(W8A8Args a, const int8_t* Xq, const float* x_scales, void* stream) {

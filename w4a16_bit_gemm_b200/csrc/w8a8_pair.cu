@@ -195,12 +195,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub>::kThread
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
         tc_fence_before();
     }
-    if (a.offsets) pdl_wait_prior();
     build_tiles(a.offsets, a.E, a.R, p.step, off, cum, warp_part, S::kThreads, a.status);  // ends with __syncthreads
-    // Only now may the next kernel start: it could take the tensor memory that
-    // this one still has to allocate, and wait for it.  With experts it starts
-    // once this one has ended (launch_shape).
-    if (!a.offsets) pdl_launch_dependents();
     cluster_arrive();
     cluster_wait();  // both CTAs' barriers are initialised, both have their tensor memory
     tc_fence_after();
@@ -213,8 +208,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub>::kThread
         const bool one = elect_one();
         const uint32_t a0 = smem_u32(smem_a), b0 = smem_u32(smem_b);
         const uint32_t full0 = map_rank(smem_u32(bar.full), 0);  // the leader's
-        int it = 0, ahead = 0;
-        bool waited = a.offsets != nullptr;
+        int it = 0;
         for (int t = worker; t < total && !__any_sync(0xffffffffu, *abort_flag); t += workers) {
             const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
             const int half = ceil_div(w.n, 32) * 16;  // rows this CTA brings
@@ -233,28 +227,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub>::kThread
                         tma_load_3d_pair(one, dst + at * atom_bytes, map, full0 + 8 * s, (kb * kAtoms + at) * kKB, row, 0);
                 }
             };
-            if (!waited) {
-                // one weight matrix: what does not depend on the previous kernel goes first
-                ahead = min(kStages, nkb);
-                for (int i = 0; i < ahead; ++i) {
-                    expect(i, i);
-                    load(a0 + i * kAtoms * kATile, kATile, &tmap_w, i, i, wrow);
-                }
-                prefetch_tmap(tx);
-                pdl_wait_prior();
-                waited = true;
-            }
             for (int kb = 0; kb < nkb; ++kb, ++it) {
                 const int s = it % kStages;
-                if (it >= ahead) {
-                    if (it >= kStages &&
-                        !__all_sync(0xffffffffu, mbar_wait(&bar.empty[s], (uint32_t)(it / kStages - 1) & 1u, a.status))) {
-                        atomicExch(&bar.abort_flag, 1);
-                        break;
-                    }
-                    expect(s, kb);
-                    load(a0 + s * kAtoms * kATile, kATile, &tmap_w, s, kb, wrow);
+                if (it >= kStages &&
+                    !__all_sync(0xffffffffu, mbar_wait(&bar.empty[s], (uint32_t)(it / kStages - 1) & 1u, a.status))) {
+                    atomicExch(&bar.abort_flag, 1);
+                    break;
                 }
+                expect(s, kb);
+                load(a0 + s * kAtoms * kATile, kATile, &tmap_w, s, kb, wrow);
                 load(b0 + s * kAtoms * kBTile, half * kKB, tx, s, kb, xrow);
             }
         }
@@ -270,7 +251,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub>::kThread
         __syncwarp();
     } else if (warp == 1) {
         // ---------------- MMA warp (leader) ----------------
-        if (!a.offsets) pdl_wait_prior();  // the bounded waits below do not cover the previous kernel
         if (rank == 0) {
             const bool one = elect_one();
             int it = 0, ti = 0;
@@ -323,7 +303,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub>::kThread
         const int et = threadIdx.x - 64;
         const int part = ((warp - 2) >> 2) & 1;                  // which half of the 64-column groups
         const int j = kSub == 1 ? 0 : (warp - 2) / kEpiWarps;    // which 128 of the CTA's channels
-        if (!a.offsets) pdl_wait_prior();
         int ti = 0;
         for (int t = worker; t < total; t += workers, ++ti) {
             const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 32);
@@ -373,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub>::kThread
 int max_of(int a, int b) { return a > b ? a : b; }
 
 template <int kSub>
-cudaError_t launch_shape(const W8A8Args& a, int step, int pairs, bool pdl, cudaStream_t stream) {
+cudaError_t launch_shape(const W8A8Args& a, int step, int pairs, cudaStream_t stream) {
     using S = Shape<kSub>;
     PairPlan p = {};
     p.step = step;
@@ -400,21 +379,14 @@ cudaError_t launch_shape(const W8A8Args& a, int step, int pairs, bool pdl, cudaS
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = (size_t)pair_smem<kSub>(a.E);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    // With experts the kernel neither starts before the one ahead has ended nor
-    // lets the next one in: a quantizer's many blocks beside it are not worth
-    // the gain (64 experts of 2048 x 4096, 8192 rows from bf16: 133.0 us a pair with
-    // the overlap, 133.7 without).
-    attr[0].val.programmaticStreamSerializationAllowed = pdl && !a.offsets ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    // No programmatic dependent launch, on either side: the kernel starts once the
+    // one ahead has ended and the next one starts once this one has.
     return cudaLaunchKernelEx(&cfg, kernel, tx, tw, a, p);
 }
 
 }  // namespace
 
-cudaError_t launch_w8a8_pair(const W8A8Args& a, int num_sms, bool pdl, cudaStream_t stream) {
+cudaError_t launch_w8a8_pair(const W8A8Args& a, int num_sms, cudaStream_t stream) {
     // Channels and rows per tile, by the time of all waves.  A k atom of a tile
     // takes as long as its reads from L2 (per CTA 128 bytes per channel, 64 per
     // row) or as its MMAs, 124 of those bytes per row and 256 channels of the
@@ -440,7 +412,7 @@ cudaError_t launch_w8a8_pair(const W8A8Args& a, int num_sms, bool pdl, cudaStrea
                 step = rows;
             }
         }
-    return sub == 1 ? launch_shape<1>(a, step, pairs, pdl, stream) : launch_shape<2>(a, step, pairs, pdl, stream);
+    return sub == 1 ? launch_shape<1>(a, step, pairs, stream) : launch_shape<2>(a, step, pairs, stream);
 }
 
 }  // namespace wq
