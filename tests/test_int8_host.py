@@ -176,3 +176,12 @@ def test_pair_kernel_never_runs_beside_another():
     src = re.sub(r"//[^\n]*", "", src)
     for word in ("pdl_launch_dependents", "pdl_wait_prior", "griddepcontrol", "ProgrammaticStreamSerialization"):
         assert word not in src, word
+
+
+def test_pair_kernel_waits_for_its_last_arrivals():
+    """Both CTAs stay until the last commits have arrived on their own barriers,
+    the leader also until both CTAs' last copies have."""
+    body = kernel_source("w8a8_pair.cu", "w8a8_pair_kernel(")
+    loop = body[body.index("for (int j = max(0, it - kStages); j < it; ++j) {"):]
+    loop = loop[:loop.index("__syncwarp();")]
+    assert re.search(r"if \(rank == 0\) mbar_wait\w*\(&bar\.full\[.*?; mbar_wait\w*\(&bar\.empty\[", loop), loop

@@ -240,13 +240,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub>::kThread
             }
         }
         // before the pair ends, the loads in flight (of both CTAs) land in the
-        // leader's count and the leader's last arrivals reach the other CTA
+        // leader's count and the leader's last arrivals reach both CTAs
         for (int j = max(0, it - kStages); j < it; ++j) {
             const uint32_t parity = (uint32_t)(j / kStages) & 1u;
-            if (rank == 0)
-                mbar_wait(&bar.full[j % kStages], parity, a.status);
-            else
-                mbar_wait(&bar.empty[j % kStages], parity, a.status);
+            if (rank == 0) mbar_wait(&bar.full[j % kStages], parity, a.status);
+            mbar_wait(&bar.empty[j % kStages], parity, a.status);
         }
         __syncwarp();
     } else if (warp == 1) {
