@@ -185,3 +185,10 @@ def test_pair_kernel_waits_for_its_last_arrivals():
     loop = body[body.index("for (int j = max(0, it - kStages); j < it; ++j) {"):]
     loop = loop[:loop.index("__syncwarp();")]
     assert re.search(r"if \(rank == 0\) mbar_wait\w*\(&bar\.full\[.*?; mbar_wait\w*\(&bar\.empty\[", loop), loop
+
+
+def test_partials_of_other_ctas_are_acquired_from_the_cluster():
+    """st.async signals at cluster scope: so does the wait ahead of the reads."""
+    body = kernel_source("w8a8_stream.cu", "w8a8_stream_kernel(")
+    in_order(body, "st_async_v4(", "mbar_wait_cluster(&bar.recv,", "recv[(s * pitch + g) * kCh + ch]")
+    assert "mbar_wait(&bar.recv" not in body

@@ -65,6 +65,34 @@ __device__ __forceinline__ void st_async_v4(uint32_t cluster_addr, uint32_t v0, 
                  : "memory");
 }
 
+// Bounded wait on an mbarrier that another CTA of the cluster arrives on, or
+// whose bytes or commits come from one: what that CTA wrote before is seen
+// (mbar_wait acquires from this CTA's own threads only).
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t* status) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        for (int i = 0; i < 16; ++i)
+            if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            raise_flag(status, kFlagTimeout);
+            return false;
+        }
+    }
+}
+
 // 3-D tiled load global -> shared, completion counted on `bar` (bytes).
 __device__ __forceinline__ void tma_load_3d(bool one, uint32_t smem_dst, const void* tmap, uint32_t bar, int32_t x,
                                             int32_t y, int32_t z) {

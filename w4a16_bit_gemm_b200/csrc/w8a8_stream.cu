@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
                         }
                     }
                 }
-                if (!__all_sync(0xffffffffu, mbar_wait(&bar.recv, 0u, a.status))) {
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(&bar.recv, 0u, a.status))) {
                     atomicExch(&bar.abort_flag, 1);
                     continue;
                 }
