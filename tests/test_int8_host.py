@@ -192,3 +192,11 @@ def test_partials_of_other_ctas_are_acquired_from_the_cluster():
     body = kernel_source("w8a8_stream.cu", "w8a8_stream_kernel(")
     in_order(body, "st_async_v4(", "mbar_wait_cluster(&bar.recv,", "recv[(s * pitch + g) * kCh + ch]")
     assert "mbar_wait(&bar.recv" not in body
+
+
+def test_pair_kernel_acquires_from_the_cluster():
+    """Every barrier but the leader's own last one is completed by the other
+    CTA's copies, commits or arrivals."""
+    body = kernel_source("w8a8_pair.cu", "w8a8_pair_kernel(")
+    assert re.findall(r"mbar_wait\((&bar\.\w+)", body) == ["&bar.drain"]
+    assert len(re.findall(r"mbar_wait_cluster\(&bar\.(?:full|empty|acc_full|acc_empty)\[", body)) == 6

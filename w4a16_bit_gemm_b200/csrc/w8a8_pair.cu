@@ -204,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub>::kThread
             for (int kb = 0; kb < nkb; ++kb, ++it) {
                 const int s = it % kStages;
                 if (it >= kStages &&
-                    !__all_sync(0xffffffffu, mbar_wait(&bar.empty[s], (uint32_t)(it / kStages - 1) & 1u, a.status))) {
+                    !__all_sync(0xffffffffu, mbar_wait_cluster(&bar.empty[s], (uint32_t)(it / kStages - 1) & 1u, a.status))) {
                     atomicExch(&bar.abort_flag, 1);
                     break;
                 }
@@ -217,8 +217,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub>::kThread
         // leader's count and the leader's last arrivals reach both CTAs
         for (int j = max(0, it - kStages); j < it; ++j) {
             const uint32_t parity = (uint32_t)(j / kStages) & 1u;
-            if (rank == 0) mbar_wait(&bar.full[j % kStages], parity, a.status);
-            mbar_wait(&bar.empty[j % kStages], parity, a.status);
+            if (rank == 0) mbar_wait_cluster(&bar.full[j % kStages], parity, a.status);
+            mbar_wait_cluster(&bar.empty[j % kStages], parity, a.status);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -236,7 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<kSub>::kThread
                 bool ok = true;
                 for (int kb = 0; ok && kb < nkb; ++kb, ++it) {
                     const int s = it % kStages;
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bar.full[s], (uint32_t)(it / kStages) & 1u, a.status));
+                    ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bar.full[s], (uint32_t)(it / kStages) & 1u, a.status));
                     const uint64_t ad = sw128_kmajor_desc(smem_u32(smem_a + s * kAtoms * kATile));
                     const uint64_t bd = sw128_kmajor_desc(smem_u32(smem_b + s * kAtoms * kBTile));
                     const int here = min(kAtoms, atoms - kb * kAtoms);
