@@ -90,11 +90,9 @@ wq_status wq_quantize_tokens(const void* X_bf16, int64_t T, int64_t d_in, const 
  *   d_in         a multiple of 32, 32 .. WQ_INT8_MAX_D_IN.
  *   Y            [M][d_out] output, y_dtype as wq_linear_w4a16.  16-byte aligned.
  *                May not overlap the inputs.
- * A call may read qweight and scales_fp16 before the kernel ahead of it on the
- * stream has ended, if that kernel allows its successor to start early
- * (programmatic dependent launch: this library's linear layers and
- * wq_quantize_tokens do; none of them writes weights).
- * Everything else is read, and Y written, after the work ahead has ended.
+ * All arrays are read, and Y written, after the work ahead on the stream has
+ * ended, also where the kernels ahead let their successors start early
+ * (programmatic dependent launch).
  * Errors: WQ_ERR_INVALID_ARG as above; WQ_ERR_UNSUPPORTED for a product of
  * more than 2^30 output tiles; WQ_ERR_CUDA if a launch fails.
  * Device flags: WQ_DEVFLAG_TIMEOUT if a pipeline wait inside the kernel gave

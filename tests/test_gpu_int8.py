@@ -826,3 +826,70 @@ def test_binding_refuses():
     for call in bad:
         with pytest.raises(ValueError):
             call()
+
+
+# ---------------------------------------------------------------------------
+# Weights written on the stream shortly before
+# ---------------------------------------------------------------------------
+
+_WRITE_LATE = r'''
+extern "C" __global__ void write_late(int* words, int value, int n) {
+    // lets the next kernel start at once, then writes after about 100 us
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const long long t0 = clock64();
+    while (clock64() - t0 < 200000) {}
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) words[i] = value;
+}
+'''
+
+
+@pytest.mark.parametrize("between", ["quantizer", "product", "w4a16"])
+@pytest.mark.parametrize("M", [1, 20, 200])
+def test_weights_written_two_kernels_ahead(M, between):
+    """A kernel that starts its successors early writes the weights; behind it
+    come the quantizer, a product with other weights or a 4-bit layer, all of
+    which do the same, then the product."""
+    b = _b()
+    N, K = 600, 2048
+    write = torch.cuda._compile_kernel(_WRITE_LATE, "write_late")
+    _, _, other, ws = operands(1, N, K, 5)
+    held = torch.zeros(N, K // 4, dtype=torch.int32, device="cuda")
+    p, q = b.PackedLinearW8(held, torch.from_numpy(ws).cuda(), N, K, K), dense(other, ws)
+    X = activations(M, K, 6)
+    xq, xs, _ = ref.quantize_tokens(X)
+    X, x = X.cuda(), tokens(xq, xs)
+    out = torch.empty(M, N, dtype=torch.float32, device="cuda")
+    p4 = b.quantize_rtn(torch.randn(N, K, device="cuda").to(torch.bfloat16))
+    b.linear_w8a8(X, q, out=out)  # the kernels are loaded
+    b.linear_w4a16(X, p4)
+    torch.cuda.synchronize()
+    for code in (1, 2, 3):
+        write(grid=(64, 1, 1), block=(256, 1, 1), args=[held, code * 0x01010101, held.numel()])
+        if between == "product":
+            b.linear_w8a8(x, q, out=out)
+        elif between == "w4a16":
+            b.linear_w4a16(X, p4)
+        y = b.linear_w8a8(X if between == "quantizer" else x, p, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        ref.check(y, *ref.product(xq, xs, np.full((N, K), code, np.int8), ws))
+
+
+def test_weights_quantized_just_ahead():
+    """New weights into the same buffer, quantizer and product, no wait of the host between."""
+    b = _b()
+    N, K = 520, 2080
+    g = torch.Generator().manual_seed(12)
+    X = activations(9, K, 2)
+    xq, xs, _ = ref.quantize_tokens(X)
+    Ws = [(torch.randn(N, K, generator=g) * 0.02).to(torch.bfloat16) for _ in range(4)]
+    X, dev = X.cuda(), [W.cuda() for W in Ws]
+    p = b.quantize_w8(dev[0])
+    torch.cuda.synchronize()
+    got = []
+    for W in dev:
+        b.quantize_w8(W, out=p)
+        got.append(b.linear_w8a8(X, p, out_dtype=torch.float32))
+    torch.cuda.synchronize()
+    for W, y in zip(dev, got):
+        q = b.quantize_w8(W)
+        ref.check(y, *ref.product(xq, xs, q.qweight.cpu().view(torch.int8).numpy(), q.scales.cpu().numpy()[:, 0]))

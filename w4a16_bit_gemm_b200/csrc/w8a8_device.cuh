@@ -118,6 +118,16 @@ __device__ __forceinline__ void tma_load_3d(bool one, uint32_t smem_dst, const v
         : "memory");
 }
 
+// The same box into L2 only.  L2 is where all SMs' writes meet, so what another
+// kernel writes there later is still read fresh.
+__device__ __forceinline__ void tma_prefetch_3d(bool one, const void* tmap, int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+        "@q cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];\n\t}" ::"l"(tmap),
+        "r"(x), "r"(y), "r"(z), "r"((int)one)
+        : "memory");
+}
+
 // named_sync that tells every thread whether `go` held in all of them: warps
 // that may have given up at different times leave a loop together.
 __device__ __forceinline__ bool named_sync_and(int id, int nthreads, bool go) {

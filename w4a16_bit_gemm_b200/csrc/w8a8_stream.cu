@@ -17,10 +17,15 @@
 // and adds up its own.  Integer sums do not depend on their order, so the
 // result is the same for every split.
 //
-// For one weight matrix, the first weights are requested before the wait for
-// the previous kernel (programmatic dependent launch): they do not depend on
-// it, the activations do.  What follows the wait is kept short: one load of
-// the rows, the MMAs, one exchange.  Every wait is bounded
+// For one weight matrix, a ring's worth of the first weights is brought into L2
+// before the wait for the previous kernel (programmatic dependent launch).  All
+// loads follow the wait: the kernels between this one and the writer of its
+// weights may have started early too, so that "the kernel ahead does not write
+// weights" does not mean that they are written.  Weights loaded into shared
+// memory before the wait saved 0.5 us more (4096 x 4096, 1 row 5.75 against 6.3)
+// and were stale behind such a chain; without any prefetch it takes 2.2 us more
+// (quantizer and product 9.0 us against 7.6).  What follows the wait is kept
+// short: one load, the MMAs, one exchange.  Every wait for memory is bounded
 // (WQ_DEVFLAG_TIMEOUT).
 //
 // Measured (weights from HBM, launches back to back): 4096 x 4096 5.75 us for
@@ -143,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
         // ---------------- copy warp ----------------
         const bool one = elect_one();
         const uint32_t a0 = smem_u32(smem_a), b0 = smem_u32(smem_b), full0 = smem_u32(bar.full);
-        int it = 0, ahead = 0;
+        int it = 0;
         bool waited = a.offsets != nullptr;
         for (int t = worker; t < total && !__any_sync(0xffffffffu, *abort_flag); t += workers) {
             const TokenTile w = find_tile(t, p.n_ct, a.E, off, cum, 16);
@@ -163,11 +168,14 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
                 }
             };
             if (!waited) {
-                // one weight matrix: what does not depend on the previous kernel goes first
-                ahead = min(p.stages, kb1 - kb0);
-                for (int i = 0; i < ahead; ++i) {
-                    expect(i, kb0 + i);
-                    load(a0 + i * p.atoms * kATile, kATile, &tmap_w, i, kb0 + i, wrow);
+                // one weight matrix: the first weights come into L2 meanwhile
+                for (int i = kb0; i < min(kb0 + p.stages, kb1); ++i) {
+                    if (whole) {
+                        tma_prefetch_3d(one, &tmap_w, 0, wrow, i * p.atoms);
+                    } else {
+                        for (int at = 0; at < p.atoms && i * p.atoms + at < atoms; ++at)
+                            tma_prefetch_3d(one, &tmap_w, (i * p.atoms + at) * kAtom, wrow, 0);
+                    }
                 }
                 prefetch_tmap(tx);
                 pdl_wait_prior();
@@ -175,15 +183,13 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
             }
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % p.stages;
-                if (it >= ahead) {
-                    if (it >= p.stages &&
-                        !__all_sync(0xffffffffu, mbar_wait(&bar.empty[s], (uint32_t)(it / p.stages - 1) & 1u, a.status))) {
-                        atomicExch(&bar.abort_flag, 1);
-                        break;
-                    }
-                    expect(s, kb);
-                    load(a0 + s * p.atoms * kATile, kATile, &tmap_w, s, kb, wrow);
+                if (it >= p.stages &&
+                    !__all_sync(0xffffffffu, mbar_wait(&bar.empty[s], (uint32_t)(it / p.stages - 1) & 1u, a.status))) {
+                    atomicExch(&bar.abort_flag, 1);
+                    break;
                 }
+                expect(s, kb);
+                load(a0 + s * p.atoms * kATile, kATile, &tmap_w, s, kb, wrow);
                 load(b0 + s * p.atoms * b_tile, rows * kAtom, tx, s, kb, w.row0);
             }
         }
@@ -243,7 +249,6 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
             const int acc = ti & 1;
             const int c = w.ct * kCh + ch;
             const bool cv = c < a.N;
-            const float sw = cv ? __half2float(__ushort_as_half(a.ws[(int64_t)w.e * a.N + c])) : 0.0f;
             // groups of 4 columns: group g belongs to CTA g % split of the cluster
             const int groups = (w.n + 3) >> 2;
             const int pitch = (groups + p.split - 1) / p.split;  // groups kept per sender
@@ -257,6 +262,7 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
                 pdl_wait_prior();
                 waited = true;
             }
+            const float sw = cv ? __half2float(__ushort_as_half(a.ws[(int64_t)w.e * a.N + c])) : 0.0f;
             float* rs = row_scale + acc * p.nt;
             if (et < w.n) rs[et] = a.xs[w.row0 + et];
             if (!named_sync_and(1, 128, !*abort_flag)) break;
