@@ -200,3 +200,12 @@ def test_pair_kernel_acquires_from_the_cluster():
     body = kernel_source("w8a8_pair.cu", "w8a8_pair_kernel(")
     assert re.findall(r"mbar_wait\((&bar\.\w+)", body) == ["&bar.drain"]
     assert len(re.findall(r"mbar_wait_cluster\(&bar\.(?:full|empty|acc_full|acc_empty)\[", body)) == 6
+
+
+def test_stream_kernel_holds_no_tensor_memory_before_the_work_ahead_with_experts():
+    """With experts: the wait, the allocation, and only then the next kernel's
+    start.  With one matrix: the allocation, then the next kernel's start."""
+    body = kernel_source("w8a8_stream.cu", "w8a8_stream_kernel(")
+    in_order(body, "if (a.offsets) pdl_wait_prior();", "tmem_alloc(", "build_tiles(", "pdl_launch_dependents();",
+             "tmem_dealloc(")
+    assert body.count("tmem_alloc(") == 1 and body.count("pdl_launch_dependents();") == 1

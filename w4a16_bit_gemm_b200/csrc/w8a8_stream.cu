@@ -128,12 +128,14 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
         bar.abort_flag = 0;
         fence_mbar_init();
     }
+    // With experts the tiles come from the work ahead: nothing is held before it has ended.
+    if (a.offsets) pdl_wait_prior();
     if (warp == 1) {
+        __syncwarp();
         tmem_alloc(&bar.tmem_slot, (uint32_t)tmem_cols);
         tmem_relinquish();
         tc_fence_before();
     }
-    if (a.offsets) pdl_wait_prior();
     build_tiles(a.offsets, a.E, a.R, p.nt, off, cum, warp_part, kThreads, a.status);  // ends with __syncthreads
     // Only now may the next kernel start: it could take the tensor memory that
     // this one still has to allocate, and wait for it.
@@ -346,6 +348,7 @@ __global__ void __launch_bounds__(kThreads) w8a8_stream_kernel(const __grid_cons
         }
     }
     if (warp == 1) {
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem_base, (uint32_t)tmem_cols);
     }
