@@ -73,8 +73,8 @@ wq_status status_of(cudaError_t e) {
 cudaError_t run_product(const W8A8Args& a, int num_sms, cudaStream_t stream) {
     const int64_t experts = a.E < a.R ? a.E : a.R;
     const int pairs = num_sms / 2;
-    const int64_t n_ct = (a.N + 255) / 256;
-    const bool few_tiles = a.offsets ? (experts + a.R / 256) * n_ct < pairs / 4 : (a.R + 31) / 32 * n_ct < pairs;
+    const int64_t n_ct = ((int64_t)a.N + 255) / 256;
+    const bool few_tiles = a.offsets ? (experts + a.R / 256) * n_ct < pairs / 4 : ((int64_t)a.R + 31) / 32 * n_ct < pairs;
     const bool streams = a.R <= 64 * experts || (few_tiles && a.K >= 2048);
     return streams ? launch_w8a8_stream(a, num_sms, pdl_enabled(), stream) : launch_w8a8_pair(a, num_sms, stream);
 }
