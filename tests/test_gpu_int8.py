@@ -148,7 +148,7 @@ def test_tokens_smoothed_and_gathered(K):
 
 @pytest.mark.parametrize("R,K", [(2371, 2080), (2400, 4096), (1190, 4128), (1200, 8192), (601, 11008), (700, 16384)])
 def test_tokens_smoothed_many_rows(R, K):
-    """Blocks that walk many rows: ordinary ones, zeros, non-finite and tiny ones,
+    """Many rows at once: ordinary ones, zeros, non-finite and tiny ones,
     gathered ones, smoothing scales of 0 and near the largest bf16."""
     g = torch.Generator().manual_seed(R)
     X = activations(R, K, 17)
@@ -167,7 +167,7 @@ def test_tokens_smoothed_many_rows(R, K):
     check_tokens(X, smooth=smooth)
 
 
-# 148 SMs: both sides of the row counts where a block gets fewer registers or a row fewer threads
+# 148 SMs: both sides of the row counts where one more block per SM is needed
 @pytest.mark.parametrize("R,K", [(592, 8192), (593, 8192), (740, 8192), (741, 8192), (1185, 4096), (1481, 2080),
                                  (148, 20000), (149, 20000), (296, 11008), (297, 11008)])
 def test_tokens_row_counts(R, K):
@@ -467,8 +467,8 @@ def test_grouped_skewed_prompt():
     check_grouped(rng.multinomial(1500, rng.dirichlet(np.full(24, 0.4))).tolist(), 640, 512, 7)
 
 
-# up to 128 rows per expert on average, in more than one wave of tiles: experts
-# below, at and above a tile's 160 rows, depths on both sides of the ring's length
+# more than one wave of tiles: experts with a part of a tile's 256 rows, with
+# several tiles and with none, depths on both sides of the ring's length
 @pytest.mark.parametrize("K", [32, 1024, 1056, 2304])
 @pytest.mark.parametrize("counts", [[70] * 40, [0, 161, 159, 160, 1, 321, 96, 0, 0, 200] * 5, [5000] + [0] * 39,
                                     [3] * 39 + [2900]])
