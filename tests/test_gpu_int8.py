@@ -33,6 +33,9 @@ def activations(R, K, seed, spread=True):
     return x.to(torch.bfloat16)
 
 
+UBF16_FP32 = (1 + ref.UBF16) * (1 + ref.U32) - 1  # an fp32 rounding, then one to bf16
+
+
 def operands(R, N, K, seed, E=None):
     """Random codes over the whole int8 range, fp16 weight scales, fp32 row scales."""
     rng = np.random.default_rng(seed)
@@ -376,6 +379,43 @@ def test_linear_whole_path_from_bf16():
     ref.check(one, y, y64)
     two = b.linear_w8a8(b.quantize_tokens(X.cuda(), smooth=smooth.cuda()), p, out_dtype=torch.float32)
     assert torch.equal(one, two)
+
+
+def test_linear_smoothed_path_approximates_the_product():
+    """SmoothQuant from end to end: X / smooth against W diag(smooth), both in 8
+    bits, bounded against X W^T; the same without smoothing is worse where a few
+    channels are loud."""
+    b = _b()
+    M, N, K = 40, 300, 1056
+    g = torch.Generator().manual_seed(21)
+    X = torch.randn(M, K, generator=g)
+    X[:, torch.randperm(K, generator=g)[:5]] *= 60
+    X = X.to(torch.bfloat16)
+    W = (torch.randn(N, K, generator=g) * 0.02).to(torch.bfloat16)
+    x64, w64 = X.double().numpy(), W.double().numpy()
+    want = x64 @ w64.T
+    smooth = (X.float().abs().amax(0) / W.float().abs().amax(0)).sqrt().to(torch.bfloat16)  # alpha = 1/2
+    rms = {}
+    for name, s in (("smoothed", smooth), ("plain", None)):
+        fold = W if s is None else (W.float() * s.float()).to(torch.bfloat16)
+        p = b.quantize_w8(fold.cuda())
+        y = b.linear_w8a8(X.cuda(), p, smooth=None if s is None else s.cuda(), out_dtype=torch.float32)
+        # A code is off by half a step (and the quotient's rounding, 2^-24 of at
+        # most 127 steps); smoothing and folding round each value to bf16 once
+        # (2^-8 of it; the quotient and the product in fp32 before that, 2^-24).
+        d = 1.0 if s is None else s.double().numpy()[None, :]
+        rounded = 0.0 if s is None else UBF16_FP32
+        xs = b.quantize_tokens(X.cuda(), smooth=None if s is None else s.cuda()).scales.cpu().double().numpy()
+        ws = p.scales.cpu().double().numpy()[:, 0]
+        half = 0.5 + 127 * 2.0 ** -23
+        a, c = np.abs(x64) / d, np.abs(w64) * d
+        da, dc = xs[:, None] * half + rounded * a, ws[:, None] * half + rounded * c
+        bound = da @ c.T + a @ dc.T + da @ dc.T
+        err = np.abs(y.cpu().double().numpy() - want)
+        # the sum's own three fp32 roundings, of a value within `bound` of the product's
+        assert np.all(err <= bound + 3.001 * ref.U32 * (np.abs(want) + bound))
+        rms[name] = float(np.sqrt((err ** 2).mean()))
+    assert rms["smoothed"] < rms["plain"], rms
 
 
 def check_linear_bf16(M, N, K, seed=0, dtype=torch.bfloat16, smooth=False, X=None):
