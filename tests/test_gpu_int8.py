@@ -516,6 +516,12 @@ def test_grouped_medium_loads(counts, K):
     check_grouped(counts, 648, K, len(counts) + K, torch.float32 if K % 128 else torch.bfloat16, before=3, behind=5)
 
 
+@pytest.mark.parametrize("counts", [[255, 256, 257, 511, 512, 513, 0, 1] * 4, [256] * 26, [513, 767, 769, 0] * 5])
+def test_grouped_tile_borders(counts):
+    """Experts at the borders of a tile's 256 rows, in more than one wave."""
+    check_grouped(counts, 648, 160, len(counts), before=1, behind=2)
+
+
 def test_grouped_from_bf16_chain_at_full_size():
     """Quantizer and loaded experts in a row, many times without a wait between."""
     b = _b()
