@@ -245,6 +245,15 @@ def test_tokens_smoothing_scales_of_every_size(K, exponent):
     check_tokens(X.to(torch.bfloat16), smooth=smooth.to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("exponent", [-90, -7, 0, 5, 60])
+def test_tokens_smoothing_of_every_pair_of_mantissas(exponent):
+    """One value per row: the row's scale tells which bf16 the quotient rounded to."""
+    m = 1 + torch.arange(128) / 128
+    X = torch.zeros(128, 128, 128)  # value, channel it stands in, channel
+    X[:, torch.arange(128), torch.arange(128)] = m[:, None]
+    check_tokens(X.view(-1, 128).to(torch.bfloat16), smooth=(m * 2.0 ** exponent).to(torch.bfloat16))
+
+
 def test_tokens_bad_row_index_is_flagged_and_coded_zero():
     b = _b()
     X = activations(5, 128, 11)
