@@ -64,18 +64,21 @@ wq_status status_of(cudaError_t e) {
 
 // The product of quantized rows.  Up to 64 rows per matrix (on average over the
 // experts that can have any) stream the weights; more share tiles between two
-// SMs.  Where the pairs' tiles do not give every pair one, a deep product
-// streams all the same: only that kernel splits K.  Measured, us stream / pair:
-//   64 x 8192 x 8192 18.3 / 21.0   128 x 4096 x 11008 17.2 / 23.8   256 x 2048 x 8192 13.1 / 17.5
-//   96 x 8192 x 8192 22.2 / 21.4   160 x 4096 x 4096 13.4 / 11.6    128 x 1001 x 1056 5.5 / 5.0
-//   64 experts of 2048 x 4096, 64 rows each 92.6 / 92.3, 94 rows 116 / 95
-//   2 experts, 150 rows, 512 x 4096 8.2 / 10.8; 160 rows, 4096 x 4096 16.2 / 15.0
+// SMs.  Where the pairs' tiles do not give every pair one, a product of some
+// depth streams all the same: only that kernel splits K, and it starts beside
+// the kernel ahead.  Measured, us stream / pair, and behind a quantizer:
+//   65 x 4096 x 11008   15.8 / 24.5   18.4 / 27.7     256 x 2048 x 8192   13.1 / 18.6   15.6 / 22.3
+//   128 x 4096 x 4096   10.3 / 12.5   12.1 / 15.7     192 x 4096 x 4096   13.4 / 12.7   15.5 / 16.2
+//   65 x 8192 x 8192    21.2 / 22.4   23.6 / 25.4     160 x 8192 x 8192   27.3 / 23.4   29.4 / 26.9
+//   77 x 1001 x 1056     5.1 /  6.5    7.0 /  8.9     320 x 512 x 512      6.4 /  5.3    8.2 /  7.7
+//   64 experts of 2048 x 4096, 65 rows each 93.7 / 94.2, 94 rows 114 / 98
+//   2 experts of 512 x 4096, 75 rows 8.3 / 12.3; of 4096 x 4096 15.8 / 15.4; of 512 x 1024, 65 rows 7.2 / 8.1
 cudaError_t run_product(const W8A8Args& a, int num_sms, cudaStream_t stream) {
     const int64_t experts = a.E < a.R ? a.E : a.R;
     const int pairs = num_sms / 2;
     const int64_t n_ct = ((int64_t)a.N + 255) / 256;
     const bool few_tiles = a.offsets ? (experts + a.R / 256) * n_ct < pairs / 4 : ((int64_t)a.R + 31) / 32 * n_ct < pairs;
-    const bool streams = a.R <= 64 * experts || (few_tiles && a.K >= 2048);
+    const bool streams = a.R <= 64 * experts || (few_tiles && a.K >= 1024);
     return streams ? launch_w8a8_stream(a, num_sms, pdl_enabled(), stream) : launch_w8a8_pair(a, num_sms, stream);
 }
 
