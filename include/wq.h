@@ -29,6 +29,11 @@
  * - `stream` is a cudaStream_t (NULL = the legacy default stream).  Every
  *   call is asynchronous on that stream: it returns once the work is
  *   enqueued.  Only wq_get_device_error synchronizes.
+ * - wq_linear_w4a16 and wq_linear_w8a16 with up to 16 tokens may read the
+ *   packed weights (not the activations) before the kernels ahead on the
+ *   stream have ended, where each of these lets its successor start early
+ *   (programmatic dependent launch).  No entry point that writes weights does;
+ *   a caller's kernel that writes them should do so after its writes only.
  * - Argument errors are detected on the host and returned synchronously with
  *   nothing launched.  A failed launch returns WQ_ERR_CUDA.  Conditions found
  *   on the device (non-finite input, fp16 scale overflow, a pipeline wait that

@@ -106,7 +106,7 @@ wq_status wq_linear_w8a8(const int8_t* Xq, const float* x_scales, int64_t M, con
  * wq_linear_w8a8_grouped -- the same product with one weight matrix per
  * expert over tokens sorted by expert: rows offsets[e] .. offsets[e+1] - 1 of
  * Xq are multiplied by expert e's matrix.  Experts may have no rows.  Rows
- * before offsets[0] and from offsets[E] on are neither read nor written.
+ * before offsets[0] and from offsets[E] on take no part; Y is not written there.
  *
  *   Xq, x_scales  [R][d_in] int8 and [R] fp32, as wq_linear_w8a8.
  *   R             rows of Xq and Y, 0 .. 2^31 - 1; 0 enqueues nothing.

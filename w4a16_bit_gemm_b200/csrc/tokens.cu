@@ -6,8 +6,10 @@
 // value, so a row is read once and kept in registers between its maximum and
 // its codes.  The arithmetic is in tokens_device.cuh.  Measured: 8192 x 8192
 // 34.4 us (5.9 TB/s, 89 % of the copy rate), smoothed 44 us; 16384 x 11008 89 us
-// (93 %); one row of 4096 1.6 us.  Issue takes about half of the cycles (10
-// instructions per value).
+// (93 %); one row of 4096 1.6 us.  Issue takes 58 % of the cycles (10
+// instructions per value), smoothed 71 % (17): there the issue slots bound it,
+// with too few warps to fill the gaps (5 blocks of 256 threads per SM at 47
+// registers), not the reciprocals' pipe (38 % busy).
 #include <stdint.h>
 
 #include "tokens_device.cuh"

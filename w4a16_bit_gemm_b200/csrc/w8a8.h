@@ -50,7 +50,7 @@ cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<uint6
 cudaError_t launch_w8a8_stream(const W8A8Args& a, int num_sms, bool pdl, cudaStream_t stream);
 
 // Many rows per weight matrix: pairs of CTAs share tiles of 256 channels x up
-// to 256 rows (w8a8_pair.cu).  Never beside the kernels around it.
+// to 256 rows (w8a8_pair.cu).  Never beside the other kernels of its stream.
 cudaError_t launch_w8a8_pair(const W8A8Args& a, int num_sms, cudaStream_t stream);
 
 }  // namespace wq

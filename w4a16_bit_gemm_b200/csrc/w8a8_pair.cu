@@ -13,18 +13,26 @@
 // of a tile runs under the products of the next.  Or both belong to one tile of
 // 512 channels, which reads a quarter less from L2 (13 to 14 TB/s into the SMs
 // was the bound of 256-channel tiles at full clock).  Persistent: each pair walks
-// the tiles in steps of the number of pairs.  Every wait is bounded
-// (WQ_DEVFLAG_TIMEOUT).
+// the tiles in steps of the number of pairs.  Every wait on an mbarrier is
+// bounded (WQ_DEVFLAG_TIMEOUT); the cluster's barriers are reached by all threads
+// on every path.
+//
+// No programmatic dependent launch, on either side: a quantizer's blocks beside
+// this kernel as it starts are the common part of three chains that did not
+// finish, when the collective allocation of tensor memory still came before the
+// first cluster barrier.  It costs 2.5 to 3 us behind a quantizer (512 x 4096 x
+// 4096 from bf16 15.1 -> 17.8 us, 128 x 11008 x 4096 15.7 -> 18.7, 512 x 8192 x
+// 8192 31.4 -> 34.0) and 1 to 4 us for a call with experts by itself.
 //
 // Bound by the tensor pipe (84 to 88 % of active cycles) and, in long runs, by
-// the power cap: 2048 x 8192 x 8192 89 us (3080 TOPS, 93 % of twice the bf16
-// rate of cuBLAS), 8192 x 28672 x 8192 1.20 to 1.23 ms in a burst, 1.33 to 1.35
-// ms back to back, 8192 x 1024 x 8192 46 us.  On the way: 1-SM tiles 153 us and
+// the power cap: 2048 x 8192 x 8192 91 us (3020 TOPS, 91 % of twice the bf16
+// rate of cuBLAS), 8192 x 28672 x 8192 1.22 to 1.24 ms in a burst, 1.33 to 1.36
+// ms back to back, 8192 x 1024 x 8192 46.5 us.  On the way: 1-SM tiles 153 us and
 // 1.82 ms; pairs 103 us and 1.37 ms; two atoms per stage and copy, so that the
 // issuing threads keep up, and an epilogue of eight warps without a test per
-// column 89 us and 1.24 ms (1.45 back to back); tiles of 512 channels.  Small
-// products add about 7 us of start, last epilogue and hand-off (512 x 8192 x
-// 8192 28.5 us).
+// column 89 us and 1.24 ms (1.45 back to back); tiles of 512 channels; waits that
+// acquire from the cluster 1 % more.  Small products add about 9 us of start,
+// last epilogue and hand-off (512 x 8192 x 8192 30 us).
 #include <stdint.h>
 
 #include "w8a8.h"
@@ -351,8 +359,7 @@ cudaError_t launch_shape(const W8A8Args& a, int step, int pairs, cudaStream_t st
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = (size_t)pair_smem<kSub>(a.E);
     cfg.stream = stream;
-    // No programmatic dependent launch, on either side: the kernel starts once the
-    // one ahead has ended and the next one starts once this one has.
+    // no launch attribute: it starts once the kernel ahead has ended (see the top)
     return cudaLaunchKernelEx(&cfg, kernel, tx, tw, a, p);
 }
 

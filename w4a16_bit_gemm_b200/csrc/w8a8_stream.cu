@@ -22,19 +22,17 @@
 // loads follow the wait: the kernels between this one and the writer of its
 // weights may have started early too, so that "the kernel ahead does not write
 // weights" does not mean that they are written.  Weights loaded into shared
-// memory before the wait saved 0.5 us more (4096 x 4096, 1 row 5.75 against 6.3)
-// and were stale behind such a chain; without any prefetch it takes 2.2 us more
-// (quantizer and product 9.0 us against 7.6).  What follows the wait is kept
-// short: one load, the MMAs, one exchange.  Every wait for memory is bounded
-// (WQ_DEVFLAG_TIMEOUT).
+// memory before the wait saved 0.6 us more (4096 x 4096, 1 row 5.75 against 6.4)
+// and were stale behind such a chain; a quantizer that lets this kernel start
+// only after its own wait took 9.0 us with it, this 7.6.  What follows the wait
+// is kept short: one load, the MMAs, one exchange.  Every wait on an mbarrier is
+// bounded (WQ_DEVFLAG_TIMEOUT).
 //
-// Measured (weights from HBM, launches back to back): 4096 x 4096 5.75 us for
-// 1 row, 6.1 for 16, 8.3 for 64; 11008 x 4096, 16 rows 11.7 us (3.9 TB/s);
-// 28672 x 8192, 1 row 39 us (6.0 TB/s, 91 % of the measured copy rate); 64
+// Measured (weights from HBM, launches back to back): 4096 x 4096 6.4 us for
+// 1 row, 6.6 for 16, 8.8 for 64; 11008 x 4096, 16 rows 11.8 us (3.9 TB/s);
+// 28672 x 8192, 1 row 39.6 us (5.9 TB/s, 90 % of the measured copy rate); 64
 // experts of 2048 x 4096, 2 rows each 84 us (97 %).  Beyond the stream itself a
-// call costs about 3 us (one matrix) to 6 us (experts: the offsets come first).
-// Codes made inside this kernel in place of a quantizer launch were slower
-// (7.4 us and more against 6.6 for both launches, 4096 x 4096, 1 row).
+// call costs about 4 us (one matrix) to 6 us (experts: the offsets come first).
 #include <stdint.h>
 
 #include "w8a8.h"
